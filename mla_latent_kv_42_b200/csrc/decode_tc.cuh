@@ -87,6 +87,7 @@ struct Ctrl {
   uint64_t s_full[2], p_free;
   // Local barriers.
   uint64_t mx_full[2][2];  // exchanges among the softmax warps: [head group][buffer xm, xh]
+  uint64_t staged;         // an item's epilogue boxes in P have been read, by all 8 softmax warps
   uint64_t f8_qk[2][2], f8_pv[2][2], f8_rope;  // FP8: an e4m3 box has landed in this CTA
   uint64_t f8_q;                               // FP8: this CTA's queries have landed
   uint64_t drain;
@@ -290,6 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
     mbar_init(bar(ctl->p_free), 1);
     for (int g2 = 0; g2 < 2; ++g2)
       for (int b2 = 0; b2 < 2; ++b2) mbar_init(bar(ctl->mx_full[g2][b2]), kSoftWarps / 2);
+    mbar_init(bar(ctl->staged), kSoftWarps);
     mbar_init(bar(ctl->drain), 2);
     for (int s = 0; s < 2; ++s)
       for (int h = 0; h < 2; ++h) {
@@ -802,6 +804,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         }
         // the O MMAs of the previous tile are done: P may be overwritten and O rescaled
         if (!wwait(ctl->p_free, (ti & 1) ^ 1)) break;
+        // a new item: the other warps' epilogue boxes, which lie in P rows of any warp, have left
+        if (c.first() && c.ii > 0 && !wwait(ctl->staged, (c.ii - 1) & 1)) break;
         if (!c.first() && __any_sync(0xffffffffu, alpha != 1.f)) {
           tc_fence_after();
           // two TMEM loads in flight per wait (one with the FP8 cache's smaller register budget)
@@ -941,7 +945,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
           }
           // the boxes have left shared memory before the next tile's softmax writes P, or before
           // the CTA exits
-          if (lane == 0) bulk_wait_read<0>();
+          if (lane == 0) {
+            bulk_wait_read<0>();
+            mbar_arrive(bar(ctl->staged));
+          }
           __syncwarp();
           tc_fence_before();
           __syncwarp();
