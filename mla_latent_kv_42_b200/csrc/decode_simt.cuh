@@ -121,14 +121,16 @@ __global__ void __launch_bounds__(256) k_lse_merge_warp(const float* __restrict_
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   const float inv = z > 0.f ? 1.f / z : 0.f;
   const float* src0 = o_part + bh * n_splits * d_c;
-  for (int c = 4 * lane; c < d_c; c += 128) {
+  for (int c0 = 0; c0 < d_c; c0 += 128) {
+    const int c = c0 + 4 * lane;
+    const bool mine = c < d_c;  // lanes without columns still take part in the shuffles below
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < n_splits; s0 += 8) {
       float4 v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        v[u] = s0 + u < n_splits ? *reinterpret_cast<const float4*>(src0 + (long)(s0 + u) * d_c + c)
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[u] = mine && s0 + u < n_splits ? *reinterpret_cast<const float4*>(src0 + (long)(s0 + u) * d_c + c)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int s = s0 + u;
@@ -139,6 +141,7 @@ __global__ void __launch_bounds__(256) k_lse_merge_warp(const float* __restrict_
         acc.w = fmaf(w, v[u].w, acc.w);
       }
     }
+    if (!mine) continue;
     T* out = o_lat + bh * d_c + c;
     Out<T>::put(out, acc.x * inv);
     Out<T>::put(out + 1, acc.y * inv);
