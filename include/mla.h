@@ -94,7 +94,13 @@ enum mla_call {
   MLA_CALL_PREFILL_ATTENTION = 4,
   MLA_CALL_LAYER_STEP_SMALL = 5,
   MLA_CALL_APPEND_KV_FP8 = 6,
-  MLA_CALL_DECODE_ATTENTION_FP8 = 7
+  MLA_CALL_DECODE_ATTENTION_FP8 = 7,
+  /* 8 names no call */
+  MLA_CALL_NORM_APPEND_KV = 9,
+  MLA_CALL_NORM_APPEND_KV_FP8 = 10,
+  MLA_CALL_READ_KV = 11,
+  MLA_CALL_READ_KV_FP8 = 12,
+  MLA_CALL_SHARED_PREFIX_ATTENTION = 13
 };
 
 /* Returns MLA_OK if every call supports `dims`, else MLA_ERR_UNSUPPORTED_DIMS or
@@ -204,8 +210,6 @@ int mla_prefill_attention(const mla_dims* dims, const void* q, const void* pool,
 int mla_out_proj(const mla_dims* dims, const void* o_lat, const void* w_uv, const void* w_o,
                  void* u, int32_t B, void* ws, size_t ws_bytes, mla_stream_t stream);
 
-/* Synchronises `stream`, returns the current device's status word in *status_out (MLA_OK or
- * the first device-side error recorded since the last read) and clears it. */
 /*
  * mla_layer_step_small — one decode step of one layer (the four calls above for one new token per
  * sequence: mla_append_kv, mla_absorb_query, mla_decode_attention, mla_out_proj) in a single
@@ -282,6 +286,81 @@ int mla_decode_attention_fp8(const mla_dims* dims, const void* q, const void* po
                              int32_t B, int32_t max_seq_len, void* o_lat, float* lse_out,
                              void* ws, size_t ws_bytes, mla_stream_t stream);
 
+/*
+ * mla_norm_append_kv — cache write of given rows, for a caller that has the projections already
+ * (a fused projection of its own, a model that normalises its latent: the RMSNorm that the
+ * published DeepSeek-V2 weights expect between W^DKV h and the cache). For each of the T tokens t,
+ * with x_t = [c (d_c) ‖ k^ (d_rope)] in row t of x, rows x_stride elements apart:
+ *   c' = c / sqrt(mean(c^2) + eps) * gain_c   (c' = c if gain_c is NULL)
+ *   k' = k^ / sqrt(mean(k^^2) + eps) * gain_r (k' = k^ if gain_r is NULL);  k^R = RoPE(k', pos[t])
+ *   pool row of (seq_idx[t], pos[t]), as in mla_append_kv  <-  [c' ‖ k^R] rounded to the element type.
+ * Everything between x and the row is fp32 (angles in double). x_stride >= d_c + d_rope, a
+ * multiple of 8; gain_c [d_c] and gain_r [d_rope] in the element type; eps > 0 and finite where a
+ * gain is given (MLA_ERR_INVALID_ARG otherwise). Any dims of mla_check_dims, one launch, no
+ * workspace. A token whose slot is outside the table or the pool is not written and records
+ * MLA_ERR_BAD_PAGE; slots of no token are left as they are. No two tokens of one call may have the
+ * same slot (which of them it holds, or parts of which, is not defined). T == 0 is a no-op.
+ */
+int mla_norm_append_kv(const mla_dims* dims, const void* x, int64_t x_stride, const void* gain_c, const void* gain_r,
+                       double eps, const int32_t* seq_idx, const int32_t* pos, const int32_t* block_table,
+                       int32_t num_seqs, int32_t max_pages, void* pool, int32_t num_pages, int32_t T,
+                       mla_stream_t stream);
+
+/* The same into an FP8 cache (the page format above, any dims): s = max|part| / 448 of the fp32
+ * parts c' and k^R (1 for an all-zero part), each byte the nearest e4m3 value (ties to even) of
+ * value / s in fp32, saturated to +-448. A NaN is stored as NaN and does not enter the maximum; an
+ * infinity makes its part's scale infinite, so that the part reads back as NaN. */
+int mla_norm_append_kv_fp8(const mla_dims* dims, const void* x, int64_t x_stride, const void* gain_c,
+                           const void* gain_r, double eps, const int32_t* seq_idx, const int32_t* pos,
+                           const int32_t* block_table, int32_t num_seqs, int32_t max_pages, void* pool,
+                           int32_t num_pages, int32_t T, mla_stream_t stream);
+
+/*
+ * mla_read_kv — the cache read back: row t of `rows` (T rows of d_c + d_rope elements, rows_stride
+ * apart: at least d_c + d_rope, a multiple of 8) is the pool's row of position pos[t] of sequence
+ * seq_idx[t]. The pairs may come in any order and more than once. With positions that fill whole
+ * pages, `rows` is a run of pages: mla_read_kv_fp8 so turns a prefix of an FP8 cache into pages
+ * that the element-type calls read. A token whose slot is outside the table or the pool gets a row
+ * of zeros and records MLA_ERR_BAD_PAGE. `rows` must not overlap the pool. T == 0 is a no-op.
+ */
+int mla_read_kv(const mla_dims* dims, const void* pool, int32_t num_pages, const int32_t* seq_idx, const int32_t* pos,
+                const int32_t* block_table, int32_t num_seqs, int32_t max_pages, void* rows, int64_t rows_stride,
+                int32_t T, mla_stream_t stream);
+
+/* The same from an FP8 cache (any dims): each value is its scale times its e4m3 value in fp32,
+ * rounded to the element type. */
+int mla_read_kv_fp8(const mla_dims* dims, const void* pool, int32_t num_pages, const int32_t* seq_idx,
+                    const int32_t* pos, const int32_t* block_table, int32_t num_seqs, int32_t max_pages, void* rows,
+                    int64_t rows_stride, int32_t T, mla_stream_t stream);
+
+/*
+ * mla_shared_prefix_attention — mla_decode_attention for a batch whose sequences begin with the
+ * same cached pages (a common system prompt or document). The outputs are those of
+ * mla_decode_attention for the same q, pool, block_table and seq_lens, to rounding; the work over
+ * the shared pages is done once for the batch where that is less: the softmax over a sequence is
+ * the join by log-sum-exp of its part over the prefix and its part over its own tokens, and for
+ * the first part all heads of all sequences are rows of one product.
+ * shared_pages int32 [num_shared_pages]: the pages of the first num_shared_pages * page_size
+ * tokens (0: nothing is shared; at most max_seq_len tokens, MLA_ERR_INVALID_ARG otherwise). Every
+ * sequence at least that long begins with these pages, and its block-table row lists them too (the
+ * call reads them from either place). A sequence that is shorter, such as an idle row of a padded
+ * batch, attends to the seq_lens[b] tokens of its own row alone.
+ * The other arguments, limits and outputs as mla_decode_attention; twice the pages of B sequences
+ * of max_seq_len must stay below 2^31. lse_out is good to fp32 where d_c = 512, d_rope = 64 and
+ * page_size = 64 or where the shape meets mla_layer_step_small's limits on heads, widths and pages:
+ * those are the shapes with kernels of their own (any head count at the first). Other shapes run as
+ * mla_decode_attention does. A bad length or page id zeroes that sequence's output (lse -inf) and
+ * records the error in the device status; a bad shared page that of every sequence that has it.
+ * ws at least mla_workspace_size(dims, MLA_CALL_SHARED_PREFIX_ATTENTION, B, max_seq_len) bytes,
+ * whatever the prefix. The result is bitwise reproducible run to run. B == 0 is a no-op.
+ */
+int mla_shared_prefix_attention(const mla_dims* dims, const void* q, const void* pool, int32_t num_pages,
+                                const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens, int32_t B,
+                                int32_t max_seq_len, const int32_t* shared_pages, int32_t num_shared_pages,
+                                void* o_lat, float* lse_out, void* ws, size_t ws_bytes, mla_stream_t stream);
+
+/* Synchronises `stream`, returns the current device's status word in *status_out (MLA_OK or
+ * the first device-side error recorded since the last read) and clears it. */
 int mla_read_device_status(mla_stream_t stream, int32_t* status_out);
 
 /* Static string for a status code. */

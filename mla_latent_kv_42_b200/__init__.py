@@ -21,11 +21,16 @@ __all__ = [
     "layer_step_small_supported", "fp8_page_bytes", "fp8_supported", "append_kv_fp8", "decode_attention_fp8",
     "CALL_APPEND_KV", "CALL_ABSORB_QUERY", "CALL_DECODE_ATTENTION", "CALL_OUT_PROJ", "CALL_PREFILL_ATTENTION",
     "CALL_LAYER_STEP_SMALL", "CALL_APPEND_KV_FP8", "CALL_DECODE_ATTENTION_FP8",
+    "norm_append_kv", "norm_append_kv_fp8", "read_kv", "read_kv_fp8", "shared_prefix_attention",
+    "CALL_NORM_APPEND_KV", "CALL_NORM_APPEND_KV_FP8", "CALL_READ_KV", "CALL_READ_KV_FP8",
+    "CALL_SHARED_PREFIX_ATTENTION",
 ]
 
 CALL_APPEND_KV, CALL_ABSORB_QUERY, CALL_DECODE_ATTENTION, CALL_OUT_PROJ, CALL_PREFILL_ATTENTION = 0, 1, 2, 3, 4
 CALL_LAYER_STEP_SMALL = 5
 CALL_APPEND_KV_FP8, CALL_DECODE_ATTENTION_FP8 = 6, 7
+CALL_NORM_APPEND_KV, CALL_NORM_APPEND_KV_FP8, CALL_READ_KV, CALL_READ_KV_FP8 = 9, 10, 11, 12
+CALL_SHARED_PREFIX_ATTENTION = 13
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
 
@@ -48,6 +53,7 @@ class _Dims(ctypes.Structure):
 
 _LIB = None
 _P, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_I64, _F64 = ctypes.c_int64, ctypes.c_double
 _SIGS = {
     "mla_check_dims": (ctypes.c_int, [_P]),
     "mla_cache_elems_per_token": (_I32, [_P]),
@@ -69,6 +75,12 @@ _SIGS = {
     "mla_fp8_supported": (ctypes.c_int, [_P]),
     "mla_append_kv_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I32, _P, _I32, _I32, _P, _SZ, _P]),
     "mla_decode_attention_fp8": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _P, _I32, _I32, _P, _P, _P, _SZ, _P]),
+    "mla_norm_append_kv": (ctypes.c_int, [_P, _P, _I64, _P, _P, _F64, _P, _P, _P, _I32, _I32, _P, _I32, _I32, _P]),
+    "mla_norm_append_kv_fp8": (ctypes.c_int, [_P, _P, _I64, _P, _P, _F64, _P, _P, _P, _I32, _I32, _P, _I32, _I32, _P]),
+    "mla_read_kv": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _P]),
+    "mla_read_kv_fp8": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _P]),
+    "mla_shared_prefix_attention": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _P,
+                                                   _SZ, _P]),
     "mla_layer_step_small": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32, _I32, _P, _P,
                                             _P, _P, _P, _SZ, _P]),
 }
@@ -359,6 +371,124 @@ def out_proj(dims, o_lat, w_uv, w_o, u=None, ws=None, stream=None):
     _check(_lib().mla_out_proj(ctypes.byref(cd), _ptr(o_lat), _ptr(w_uv), _ptr(w_o), _ptr(u), B, _ptr(ws), nbytes,
                                _stream(stream)), "mla_out_proj")
     return u
+
+
+def _args(dims, elem, named):
+    """Checks of the row and shared-prefix calls: each (tensor, name, dtype, shape) lies on the current
+    device, contiguous but for the stride of a two-dimensional row tensor's rows, with that type
+    and shape (None: any size)."""
+    import torch
+    here = torch.cuda.current_device()
+    for t, name, dtype, shape, strided in named:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+        if t.dtype != (dtype or elem):
+            raise ValueError(f"{name} must be {dtype or elem}, got {t.dtype}")
+        if t.dim() != len(shape) or any(want is not None and want != got for want, got in zip(shape, t.shape)):
+            raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, "
+                             f"got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            # rows with a stride of their own (a slice of a wider product)
+            if not strided or t.stride(1) != 1 or t.stride(0) % 8 or t.stride(0) < t.shape[1]:
+                raise ValueError(f"{name} must be contiguous" +
+                                 (" but for its rows, a multiple of 8 elements apart" if strided else ""))
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0) - t.stride(0) % 8, t.shape[1])
+
+
+def _pool_shape(dims, fp8):
+    D = dims.d_c + dims.d_rope
+    return (None, dims.page_size * (D + 8)) if fp8 else (None, dims.page_size, D)
+
+
+def _norm_append(name, fp8, dims, x, seq_idx, pos, block_table, pool, gain_c, gain_r, eps, stream):
+    import torch
+    e, i32, D = _elem(dims), torch.int32, dims.d_c + dims.d_rope
+    T = x.shape[0] if x.dim() else 0
+    named = [(x, "x", None, (None, D), True), (seq_idx, "seq_idx", i32, (T,), False), (pos, "pos", i32, (T,), False),
+             (block_table, "block_table", i32, (None, None), False),
+             (pool, "pool", torch.uint8 if fp8 else None, _pool_shape(dims, fp8), False)]
+    if gain_c is not None:
+        named.append((gain_c, "gain_c", None, (dims.d_c,), False))
+    if gain_r is not None:
+        named.append((gain_r, "gain_r", None, (dims.d_rope,), False))
+    _args(dims, e, named)
+    cd = c_dims(dims)
+    _check(getattr(_lib(), name)(ctypes.byref(cd), x.data_ptr(), _row_stride(x), _ptr(gain_c), _ptr(gain_r), eps,
+                                 seq_idx.data_ptr(), pos.data_ptr(), block_table.data_ptr(), block_table.shape[0],
+                                 block_table.shape[1], pool.data_ptr(), pool.shape[0], T, _stream(stream)), name)
+    return pool
+
+
+def norm_append_kv(dims, x, seq_idx, pos, block_table, pool, gain_c=None, gain_r=None, eps=1e-6, stream=None):
+    """mla_norm_append_kv: write rows [c ‖ k^] that the caller has (``x`` [T, d_c + d_rope], rows may be
+    strided), each part RMS-normalised where its gain is given, k^ rotated, into their slots."""
+    return _norm_append("mla_norm_append_kv", False, dims, x, seq_idx, pos, block_table, pool, gain_c, gain_r, eps,
+                        stream)
+
+
+def norm_append_kv_fp8(dims, x, seq_idx, pos, block_table, pool, gain_c=None, gain_r=None, eps=1e-6, stream=None):
+    """mla_norm_append_kv_fp8: the same into ``pool`` (uint8 [num_pages, fp8_page_bytes(dims)])."""
+    return _norm_append("mla_norm_append_kv_fp8", True, dims, x, seq_idx, pos, block_table, pool, gain_c, gain_r, eps,
+                        stream)
+
+
+def _read(name, fp8, dims, pool, seq_idx, pos, block_table, out, stream):
+    import torch
+    e, i32, D = _elem(dims), torch.int32, dims.d_c + dims.d_rope
+    T = seq_idx.shape[0] if seq_idx.dim() else 0
+    if out is None:
+        out = torch.empty((T, D), dtype=e, device=pool.device)
+    _args(dims, e, [(pool, "pool", torch.uint8 if fp8 else None, _pool_shape(dims, fp8), False),
+                    (seq_idx, "seq_idx", i32, (T,), False), (pos, "pos", i32, (T,), False),
+                    (block_table, "block_table", i32, (None, None), False), (out, "out", None, (T, D), True)])
+    cd = c_dims(dims)
+    _check(getattr(_lib(), name)(ctypes.byref(cd), pool.data_ptr(), pool.shape[0], seq_idx.data_ptr(), pos.data_ptr(),
+                                 block_table.data_ptr(), block_table.shape[0], block_table.shape[1], out.data_ptr(),
+                                 _row_stride(out), T, _stream(stream)), name)
+    return out
+
+
+def read_kv(dims, pool, seq_idx, pos, block_table, out=None, stream=None):
+    """mla_read_kv: the cached rows of the given (sequence, position) pairs, [T, d_c + d_rope]."""
+    return _read("mla_read_kv", False, dims, pool, seq_idx, pos, block_table, out, stream)
+
+
+def read_kv_fp8(dims, pool, seq_idx, pos, block_table, out=None, stream=None):
+    """mla_read_kv_fp8: the same from an FP8 cache, as element-type rows."""
+    return _read("mla_read_kv_fp8", True, dims, pool, seq_idx, pos, block_table, out, stream)
+
+
+def shared_prefix_attention(dims, q, pool, block_table, seq_lens, max_seq_len, shared_pages, o_lat=None, lse=None,
+                            want_lse=True, ws=None, stream=None):
+    """mla_shared_prefix_attention: decode_attention for a batch whose sequences begin with the pages
+    ``shared_pages`` (int32 [num_shared_pages], all full), which are attended once for the batch."""
+    import torch
+    e, i32 = _elem(dims), torch.int32
+    B = q.shape[0] if q.dim() else 0
+    if o_lat is None:
+        o_lat = torch.empty((B, dims.n_heads, dims.d_c), dtype=e, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((B, dims.n_heads), dtype=torch.float32, device=q.device)
+    named = [(q, "q", None, (None, dims.n_heads, dims.d_c + dims.d_rope), False),
+             (pool, "pool", None, _pool_shape(dims, False), False),
+             (block_table, "block_table", i32, (B, None), False), (seq_lens, "seq_lens", i32, (B,), False),
+             (shared_pages, "shared_pages", i32, (None,), False),
+             (o_lat, "o_lat", None, (B, dims.n_heads, dims.d_c), False)]
+    if lse is not None:
+        named.append((lse, "lse", torch.float32, (B, dims.n_heads), False))
+    _args(dims, e, named)
+    ws, nbytes = _ws(dims, CALL_SHARED_PREFIX_ATTENTION, B, max_seq_len, ws, q.device)
+    cd = c_dims(dims)
+    _check(_lib().mla_shared_prefix_attention(
+        ctypes.byref(cd), q.data_ptr(), pool.data_ptr(), pool.shape[0], block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), B, int(max_seq_len), shared_pages.data_ptr(), shared_pages.shape[0], o_lat.data_ptr(),
+        _ptr(lse), ws.data_ptr(), nbytes, _stream(stream)), "mla_shared_prefix_attention")
+    return o_lat, lse
 
 
 def read_device_status(stream=None) -> int:

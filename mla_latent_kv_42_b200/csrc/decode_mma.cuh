@@ -78,13 +78,19 @@ struct MmaAttnArgs {
   float* lse_out;           // [B, n_h] or null (n_splits == 1)
   float* o_part;            // [B * n_h][n_splits][d_c] (n_splits > 1)
   float* lse_part;          // [B * n_h][n_splits]
+  // attn_mma_item<T, true> (the own tokens of a batch that shares a prefix) only:
+  int B;
+  const int* first;         // [B] first token (a multiple of page_size), -1 for a rejected sequence
+  int part0;                // the item's split s writes partial part0 + s
 };
 
 // One work item: tokens [split * split_len, min(L, (split + 1) * split_len)) of sequence b, by the
 // first 128 threads of the calling CTA (four warps); `sm` holds smem_bytes(D) bytes, 16-aligned.
 // Requirements (checked by the host): n_h <= 16, D % 16 == 0, D <= 192, d_c % 16 == 0, d_c <= 128,
-// page_size % 16 == 0, split_len a multiple of 64.
-template <typename T>
+// page_size % 16 == 0, split_len a multiple of 64. kOwn: the tokens start at first[b], lengths
+// are the plan's (0 for a rejected sequence) and the denominator sums the weights before they are
+// rounded, so that the lse is good to fp32.
+template <typename T, bool kOwn = false>
 __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* sm) {
   using namespace dmma;
   using P2 = typename Pack<T>::T2;
@@ -107,12 +113,19 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
   const uint32_t sm_u32 = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
 
   int L = a.seq_lens[b];
-  bool bad_len = L < 1 || L > max_seq_len || (L + page_size - 1) / page_size > max_pages;
-  if (bad_len) {
-    if (split == 0 && tid == 0) record_error(MLA_ERR_BAD_SEQ_LEN);
-    L = 0;
+  int from = 0;
+  if constexpr (kOwn) {
+    from = max(0, a.first[b]);
+  } else {
+    bool bad_len = L < 1 || L > max_seq_len || (L + page_size - 1) / page_size > max_pages;
+    if (bad_len) {
+      if (split == 0 && tid == 0) record_error(MLA_ERR_BAD_SEQ_LEN);
+      L = 0;
+    }
   }
-  const int t0 = split * split_len, t1 = min(L, t0 + split_len);
+  const int t0 = from + split * split_len;
+  // kOwn: the last split takes all that is left (splits are sized for sequences past the prefix)
+  const int t1 = kOwn && a.part0 + split + 1 == n_splits ? L : min(L, t0 + split_len);
   const int n_stages = t1 > t0 ? (t1 - t0 + kStageTokens - 1) / kStageTokens : 0;
   const int* btb = bt + (long)b * max_pages;
   bool bad_page = false;
@@ -224,8 +237,12 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
           v[e] = pe;
         }
         const P2 p01 = Pack<T>::make(v[0], v[1]), p23 = Pack<T>::make(v[2], v[3]);
-        const float2 f01 = Pack<T>::f2(p01), f23 = Pack<T>::f2(p23);
-        lsum[h2] += (f01.x + f01.y) + (f23.x + f23.y);
+        if constexpr (kOwn) {
+          lsum[h2] += (v[0] + v[1]) + (v[2] + v[3]);
+        } else {
+          const float2 f01 = Pack<T>::f2(p01), f23 = Pack<T>::f2(p23);
+          lsum[h2] += (f01.x + f01.y) + (f23.x + f23.y);
+        }
         s[0][2 * h2] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&p01));  // reuse as packed storage
         s[1][2 * h2] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&p23));
       }
@@ -293,8 +310,9 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
       Out<T>::put(o_lat + bh * d_c + col, acc * inv);
       if (col == 0 && lse_out != nullptr) lse_out[bh] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     } else {
-      o_part[(bh * n_splits + split) * d_c + col] = acc * inv;
-      if (col == 0) lse_part[bh * n_splits + split] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      const long part = bh * n_splits + split + (kOwn ? a.part0 : 0);
+      o_part[part * d_c + col] = acc * inv;
+      if (col == 0) lse_part[part] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
 }

@@ -133,6 +133,21 @@ struct DecodeTcMaps {
   CUtensorMap o_lat_h, o_part_h;  // the same with 32-byte x 32-head boxes, unswizzled
 };
 
+// Attention over a shared prefix (see shared_prefix.cuh). The first prefix_items items are the
+// packed query rows [128 i, 128 i + 128) of the batch over the shared pages; item prefix_items + b
+// is sequence b over its own tokens [first[b], seq_lens[b]). Without prefix items the tokens are
+// the whole sequence and an item that one pair finishes goes straight to o_lat; with them every
+// result is an fp32 partial.
+struct SharedTcMaps : DecodeTcMaps {
+  CUtensorMap o_pre, o_pre_h;  // partials of the prefix items: (512 columns, 128 rows, items + C)
+};
+struct SharedTcParams : DecodeTcParams {
+  const int* first;         // [B], -1 for a rejected sequence (which has no tiles)
+  const int* shared_pages;  // pages of the prefix
+  int prefix_items, prefix_len;
+  float* lse_pre;           // [items + C][128]
+};
+
 // Tiles [t0, t1) of sequence b handled by this pair (n_b = tiles of the sequence).
 struct Item {
   int b, t0, t1, n_b;
@@ -250,10 +265,12 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t count, bool 
   return r != 0;
 }
 
-template <typename T, bool F8 = false>
+template <typename T, bool F8 = false, bool kShared = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8 : dec::kThreads, 1)
-    k_decode_tc(const __grid_constant__ DecodeTcMaps maps, const DecodeTcParams p) {
+    k_decode_tc(const __grid_constant__ std::conditional_t<kShared, SharedTcMaps, DecodeTcMaps> maps,
+                const std::conditional_t<kShared, SharedTcParams, DecodeTcParams> p) {
   using namespace dec;
+  static_assert(!(F8 && kShared), "the shared prefix is read from the element-type cache");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl* ctl = reinterpret_cast<Ctrl*>(data + kDataBytes);
@@ -335,6 +352,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
     return ok;
   };
   const uint32_t set_u32 = data_u32 + kSetOff;
+  // Item b's tokens, pages and first query row: sequence b itself, or (kShared) 128 packed rows
+  // over the shared pages or a sequence's own tokens.
+  auto item_len = [&](int b) {
+    if constexpr (kShared) {
+      if (b < p.prefix_items) return p.prefix_len;
+      return p.seq_lens[b - p.prefix_items] - p.first[b - p.prefix_items];
+    } else {
+      return p.seq_lens[b];
+    }
+  };
+  auto item_pages = [&](int b) {
+    if constexpr (kShared) {
+      if (b < p.prefix_items) return p.shared_pages;
+      b -= p.prefix_items;
+      return p.bt + (long)b * p.max_pages + p.first[b] / kPage;
+    } else {
+      return p.bt + (long)b * p.max_pages;
+    }
+  };
+  auto item_row = [&](int b) {
+    if constexpr (kShared) return b < p.prefix_items ? 128 * b : (b - p.prefix_items) * p.n_h;
+    else return b * p.n_h;
+  };
 
   if (has_work) {
     if (warp == kLoadWarp) {
@@ -353,11 +393,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         Cursor c;
         c.start(prefix, p.B, cluster, nclusters);
         int L = 0;
+        const int* btb = nullptr;
         while (c.valid) {
           const int s = c.ti & 1, b = c.item.b, t = c.t;
           // global reads first: their latency overlaps the waits below
-          if (c.first()) L = p.seq_lens[b];
-          const int* btb = p.bt + (long)b * p.max_pages;
+          if (c.first()) {
+            L = item_len(b);
+            btb = item_pages(b);
+          }
           const int page_idx = 2 * t + (int)rank;
           const int nv = min(kPage, max(0, L - kPage * page_idx));  // tokens in page r of the tile
           const int page = nv > 0 ? btb[page_idx] : 0;
@@ -365,10 +408,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
             if (!wait(ctl->q_free, (c.ii & 1) ^ 1)) break;
             if constexpr (F8) {  // the converting warps turn them into fp16 and publish them
               mbar_arrive_expect_tx(bar(ctl->f8_q), 9 * kChunk);
-              tma_load_3d(data_u32 + kQOff, &maps.q9, bar(ctl->f8_q), 0, b * p.n_h + 64 * (int)rank, 0);
+              tma_load_3d(data_u32 + kQOff, &maps.q9, bar(ctl->f8_q), 0, item_row(b) + 64 * (int)rank, 0);
             } else {
               mbar_arrive_expect_tx_cl(lead(ctl->q_full), 9 * kChunk);
-              tma_load_3d_pair(data_u32 + kQOff, &maps.q9, lead(ctl->q_full), 0, b * p.n_h + 64 * (int)rank, 0);
+              tma_load_3d_pair(data_u32 + kQOff, &maps.q9, lead(ctl->q_full), 0, item_row(b) + 64 * (int)rank, 0);
             }
           }
           if (!wait(ctl->rope_done, (c.ti & 1) ^ 1)) break;
@@ -416,13 +459,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         Cursor c;
         c.start(prefix, p.B, cluster, nclusters);
         int L = 0;
+        const int* btb = nullptr;
         const int g = 1 - (int)rank;
         while (c.valid) {
-          const int s = c.ti & 1, b = c.item.b, t = c.t;
-          if (c.first()) L = p.seq_lens[b];
+          const int s = c.ti & 1, t = c.t;
+          if (c.first()) {
+            L = item_len(c.item.b);
+            btb = item_pages(c.item.b);
+          }
           const uint32_t ph = (c.ti >> 1) & 1;
           const int nv = min(kPage, max(0, L - kTile * t - kPage * g));  // tokens in page g of the tile
-          const int page = nv > 0 ? p.bt[(long)b * p.max_pages + 2 * t + g] : 0;  // read ahead of the waits
+          const int page = nv > 0 ? btb[2 * t + g] : 0;  // read ahead of the waits
           // the O MMAs of tile ti - 2 are complete, so every barrier of set s is in this tile's phase
           if (!wait(ctl->set_free[s][1], ph ^ 1)) break;
           mbar_arrive_cl(lead(ctl->pv_full[s][(int)rank]));      // j = 0, g = r
@@ -767,7 +814,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         if (c.first()) {
           m_ref = -INFINITY;
           lsum = 0.f;
-          L = p.seq_lens[c.item.b];
+          L = item_len(c.item.b);
         }
         if (!wwait(ctl->s_full[sb], (ti >> 1) & 1)) break;
         tc_fence_after();
@@ -827,7 +874,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         }
         // P row h, tokens [32ch, 32ch + 32) of page g: p = 2^(s * scale - m_ref), one FFMA and one
         // ex2 per token. The sum of the rounded weights is the denominator (it matches what the
-        // MMA accumulates).
+        // MMA accumulates); with kShared that of the weights before rounding, so that the lse,
+        // which joins the parts of a sequence, is good to fp32 (rounded weights shift it by up to
+        // 2^-9) and o is off by the weights' own roundings alone.
         float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int u4 = 0; u4 < 4; ++u4) {
@@ -835,10 +884,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int k = 8 * u4 + 2 * e;
-            const typename Pack<PT>::T2 pr2 = Pack<PT>::make(ex2_approx(fmaf(u2f(sr[k]), p.scale_log2, -m_ref)),
-                                                           ex2_approx(fmaf(u2f(sr[k + 1]), p.scale_log2, -m_ref)));
-            const float2 back = Pack<PT>::f2(pr2);
-            sums[e] += back.x + back.y;
+            const float w0 = ex2_approx(fmaf(u2f(sr[k]), p.scale_log2, -m_ref));
+            const float w1 = ex2_approx(fmaf(u2f(sr[k + 1]), p.scale_log2, -m_ref));
+            const typename Pack<PT>::T2 pr2 = Pack<PT>::make(w0, w1);
+            if constexpr (kShared) {
+              sums[e] += w0 + w1;
+            } else {
+              const float2 back = Pack<PT>::f2(pr2);
+              sums[e] += back.x + back.y;
+            }
             w[e] = *reinterpret_cast<const uint32_t*>(&pr2);
           }
           *reinterpret_cast<uint4*>(p_row_ptr + ((((4 * ch + u4) ^ (h & 7))) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -858,8 +912,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
           const float inv = l > 0.f ? 1.f / l : 0.f;
           const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
           const Item& it = c.item;
-          const bool whole = it.t0 == 0 && it.t1 == it.n_b;
-          const long slot = (long)it.b + cluster;
+          bool whole = it.t0 == 0 && it.t1 == it.n_b, packed = false;
+          int ib = it.b, n_rows = p.n_h;  // the item among its kind, its query rows
+          if constexpr (kShared) {
+            packed = it.b < p.prefix_items;
+            whole = whole && p.prefix_items == 0;
+            if (packed) n_rows = 128;
+            else ib -= p.prefix_items;
+          }
+          const long slot = (long)ib + cluster;
           const int col0 = 256 * ch + 128 * g;  // latent columns [col0, col0 + 128)
           // The warp writes its 32 heads x 128 columns in rounds of 64 bytes per head through
           // shared memory: each lane puts its head's segment in row `lane` of a 2 KB box in the
@@ -872,6 +933,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
           const bool last_item = c.it.g >= c.it.g_end;
           const uint32_t wsw = (lane >> 1) & 3;
           const int head0 = 64 * (int)rank + 32 * (qd & 1);
+          const CUtensorMap *part_map = &maps.o_part, *part_map_h = &maps.o_part_h;
+          if constexpr (kShared) {
+            if (packed) {
+              part_map = &maps.o_pre;
+              part_map_h = &maps.o_pre_h;
+            }
+          }
           int round = 0;
           auto stage_store = [&](const uint32_t (&w)[16], int col) {
             if (!last_item) {
@@ -891,8 +959,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
                 __syncwarp();
                 if (lane == 0) {
                   const int c = col + hf * (whole ? 16 : 8);  // 32 bytes of columns
-                  if (whole) tma_store_3d(&maps.o_lat_h, box_u32, c, head0, it.b);
-                  else tma_store_3d(&maps.o_part_h, box_u32, c, head0, (int)slot);
+                  if (whole) tma_store_3d(&maps.o_lat_h, box_u32, c, head0, ib);
+                  else tma_store_3d(part_map_h, box_u32, c, head0, (int)slot);
                   bulk_commit_group();
                 }
               }
@@ -908,13 +976,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
             fence_proxy_async_cta();
             __syncwarp();
             if (lane == 0) {
-              if (whole) tma_store_3d(&maps.o_lat, stage_u32, col, head0, it.b);
-              else tma_store_3d(&maps.o_part, stage_u32, col, head0, (int)slot);
+              if (whole) tma_store_3d(&maps.o_lat, stage_u32, col, head0, ib);
+              else tma_store_3d(part_map, stage_u32, col, head0, (int)slot);
               bulk_commit_group();
             }
           };
+          // (kShared: a warp none of whose 32 rows are the item's has nothing to store)
+          const int c_end = kShared && head0 >= n_rows ? 0 : 128;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
+          for (int c0 = 0; c0 < c_end; c0 += 32) {
             uint32_t r[32];
             tmem_ld32(tmem + lane_base + kOCol + 128 * ch + c0, r);
             tmem_wait_ld();
@@ -936,11 +1006,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
               }
             }
           }
-          if (head < p.n_h && g == 0 && ch == 0) {
+          if (head < n_rows && g == 0 && ch == 0) {
             if (whole) {
-              if (p.lse_out != nullptr) p.lse_out[(long)it.b * p.n_h + head] = lse;
+              if (p.lse_out != nullptr) p.lse_out[(long)ib * p.n_h + head] = lse;
             } else {
-              p.lse_part[slot * p.n_h + head] = lse;
+              float* lse_part = p.lse_part;
+              if constexpr (kShared) {
+                if (packed) lse_part = p.lse_pre;
+              }
+              lse_part[slot * n_rows + head] = lse;
             }
           }
           // the boxes have left shared memory before the next tile's softmax writes P, or before

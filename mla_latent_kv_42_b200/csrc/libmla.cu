@@ -18,6 +18,8 @@
 #include "layer_small.cuh"
 #include "prefill.cuh"
 #include "proj_host.cuh"
+#include "rows.cuh"
+#include "shared_prefix.cuh"
 
 using namespace mla;
 
@@ -32,7 +34,8 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
-thread_local int32_t t_launches[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+constexpr int kNumCalls = MLA_CALL_SHARED_PREFIX_ATTENTION + 1;
+thread_local int32_t t_launches[kNumCalls] = {};
 // Profiling hook: events recorded around the attention kernel of this thread's decode calls.
 thread_local cudaEvent_t t_ev_before = nullptr, t_ev_after = nullptr;
 inline void mark_before(cudaStream_t st) {
@@ -182,14 +185,14 @@ int fp8_dims(const mla_dims* d) {
   return decode_tc_eligible(d) ? MLA_OK : MLA_ERR_UNSUPPORTED_DIMS;
 }
 
-template <typename T, bool F8 = false>
+template <typename T, bool F8 = false, bool kShared = false>
 bool decode_tc_set_smem() {
   static std::atomic<bool> done[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
   if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(tc::k_decode_tc<T, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc::dec::kSmem) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(tc::k_decode_tc<T, F8, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)tc::dec::kSmem) != cudaSuccess)
       return false;
     done[dev].store(true, std::memory_order_release);
   }
@@ -445,6 +448,319 @@ int prefill_impl(const mla_dims* d, const void* q, const void* pool, int32_t num
   return finish_launches(MLA_CALL_PREFILL_ATTENTION, n);
 }
 
+// ---------------------------------------------------------------- rows written and read back
+rows::SlotMap slot_map(const mla_dims* d, const int32_t* bt, int32_t num_seqs, int32_t max_pages, int32_t num_pages) {
+  return rows::SlotMap{bt, (int)num_seqs, (int)max_pages, (int)num_pages, (int)d->page_size};
+}
+
+// CTAs for T tokens, `per_warp` of them a warp at a time: one wave of eight CTAs per SM at most,
+// then the warps loop.
+unsigned rows_grid(int T, int per_warp) {
+  const long need = ((long)T + (long)rows::kWarps * per_warp - 1) / ((long)rows::kWarps * per_warp);
+  return (unsigned)std::min<long>(need, 8L * device_sm_count());
+}
+
+template <typename T, bool kFp8>
+int norm_append_impl(const mla_dims* d, const void* x, int64_t x_stride, const void* g_c, const void* g_r, double eps,
+                     const int32_t* seq_idx, const int32_t* pos, const rows::SlotMap& slot, void* pool, int32_t T_,
+                     cudaStream_t st) {
+  rows::AppendArgs a;
+  a.x = x;
+  a.x_stride = (long)x_stride;
+  a.g_c = g_c;
+  a.g_r = g_r;
+  a.eps = (float)eps;
+  a.seq_idx = seq_idx;
+  a.pos = pos;
+  a.slot = slot;
+  a.d_c = d->d_c;
+  a.D = d->d_c + d->d_rope;
+  a.T = T_;
+  a.pool = pool;
+  a.turns.table = d->rope_inv_freq;
+  double r = std::pow(d->rope_base, -2.0 / (double)d->d_rope);
+  for (int j = 0; j < rows::kPowers; ++j, r *= r) a.turns.pw[j] = r;
+  if (launch_pdl(k_norm_append<T, kFp8>, dim3(rows_grid(T_, 1)), dim3(32 * rows::kWarps), 0, st, a) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return finish_launches(kFp8 ? MLA_CALL_NORM_APPEND_KV_FP8 : MLA_CALL_NORM_APPEND_KV, 1);
+}
+
+template <bool kFp8>
+int norm_append_call(const mla_dims* d, const void* x, int64_t x_stride, const void* g_c, const void* g_r, double eps,
+                     const int32_t* seq_idx, const int32_t* pos, const int32_t* bt, int32_t num_seqs,
+                     int32_t max_pages, void* pool, int32_t num_pages, int32_t T, mla_stream_t stream) {
+  const int r = check_dims_impl(d);
+  if (r != MLA_OK) return r;
+  if (T < 0 || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (x_stride < d->d_c + d->d_rope || x_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if ((g_c || g_r) && !(eps > 0.0 && std::isfinite(eps))) return MLA_ERR_INVALID_ARG;
+  if (T == 0) {
+    t_launches[kFp8 ? MLA_CALL_NORM_APPEND_KV_FP8 : MLA_CALL_NORM_APPEND_KV] = 0;
+    return MLA_OK;
+  }
+  if (!x || !seq_idx || !pos || !bt || !pool) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(g_c) || !aligned16(g_r) || !aligned16(pool)) return MLA_ERR_ALIGNMENT;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const rows::SlotMap slot = slot_map(d, bt, num_seqs, max_pages, num_pages);
+  if (d->dtype == MLA_BF16)
+    return norm_append_impl<__nv_bfloat16, kFp8>(d, x, x_stride, g_c, g_r, eps, seq_idx, pos, slot, pool, T, st);
+  return norm_append_impl<__half, kFp8>(d, x, x_stride, g_c, g_r, eps, seq_idx, pos, slot, pool, T, st);
+}
+
+template <bool kFp8>
+int read_kv_call(const mla_dims* d, const void* pool, int32_t num_pages, const int32_t* seq_idx, const int32_t* pos,
+                 const int32_t* bt, int32_t num_seqs, int32_t max_pages, void* out, int64_t out_stride, int32_t T,
+                 mla_stream_t stream) {
+  const int r = check_dims_impl(d);
+  if (r != MLA_OK) return r;
+  if (T < 0 || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (out_stride < d->d_c + d->d_rope || out_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  const int call = kFp8 ? MLA_CALL_READ_KV_FP8 : MLA_CALL_READ_KV;
+  if (T == 0) {
+    t_launches[call] = 0;
+    return MLA_OK;
+  }
+  if (!pool || !seq_idx || !pos || !bt || !out) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(pool) || !aligned16(out)) return MLA_ERR_ALIGNMENT;
+  const rows::ReadArgs a{pool, seq_idx, pos, slot_map(d, bt, num_seqs, max_pages, num_pages), (int)d->d_c,
+                         (int)(d->d_c + d->d_rope), (int)T, out, (long)out_stride};
+  const dim3 grid(rows_grid(T, rows::kReadTokens)), block(32 * rows::kWarps);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = d->dtype == MLA_BF16 ? launch_pdl(k_read_rows<__nv_bfloat16, kFp8>, grid, block, 0, st, a)
+                                             : launch_pdl(k_read_rows<__half, kFp8>, grid, block, 0, st, a);
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  return finish_launches(call, 1);
+}
+
+// ---------------------------------------------------------------- attention over a shared prefix
+// Shapes of the tensor-core pair kernel with packed query rows: any head count.
+bool shared_tc_eligible(const mla_dims* d) {
+  return d->d_c == tc::dec::kDc && d->d_c + d->d_rope == tc::dec::kD && d->page_size == tc::dec::kPage;
+}
+
+// Whether the rows of B sequences are packed over the prefix.
+bool shared_packs(const mla_dims* d, int B) {
+  const long R = (long)B * d->n_heads;
+  if (shared_tc_eligible(d)) return (R + 127) / 128 < B;
+  return R > 16;
+}
+
+struct SharedTcLayout {
+  int Mt;  // packed row tiles
+  size_t first, len, tile_prefix, o_pre, lse_pre, o_part, lse_part, bytes;
+};
+SharedTcLayout shared_tc_layout(const mla_dims* d, int B, bool packed) {
+  SharedTcLayout L;
+  const size_t C = decode_clusters();
+  L.Mt = packed ? (int)(((long)B * d->n_heads + 127) / 128) : 0;
+  const size_t pre_rows = packed ? (L.Mt + C) * 128 : 0, own_rows = (B + C) * (size_t)d->n_heads;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  L.first = take((size_t)B * 4);
+  L.len = take((size_t)B * 4);
+  L.tile_prefix = take(((size_t)L.Mt + B + 1) * 4);
+  L.o_pre = take(pre_rows * tc::dec::kDc * 4);
+  L.lse_pre = take(pre_rows * 4);
+  L.o_part = take(own_rows * tc::dec::kDc * 4);
+  L.lse_part = take(own_rows * 4);
+  L.bytes = off;
+  return L;
+}
+
+// Splits of the warp-MMA kernel's items: the prefix of each row tile, and each sequence's own
+// tokens past it, in whole 64-token stages, about three CTAs per SM.
+struct SharedMmaPlan {
+  int row_tiles, pre_splits, pre_split_len, own_splits, own_split_len;
+};
+constexpr int kSharedMinStages = 4;  // stages of a prefix split at least
+int shared_splits(long items, long stages, long min_stages, int* split_len) {
+  long s = std::max(1L, 3L * device_sm_count() / items);
+  s = std::min(s, std::max(1L, (stages + min_stages - 1) / min_stages));
+  const long per = (stages + s - 1) / s;
+  *split_len = (int)(per * dmma::kStageTokens);
+  return (int)((stages + per - 1) / per);
+}
+SharedMmaPlan shared_mma_plan(const mla_dims* d, int B, int shared_len, int max_seq_len) {
+  SharedMmaPlan p{};
+  auto stages = [](long tokens) { return std::max(1L, (tokens + dmma::kStageTokens - 1) / dmma::kStageTokens); };
+  if (shared_len > 0) {
+    p.row_tiles = (int)(((long)B * d->n_heads + shared::kRowTile - 1) / shared::kRowTile);
+    p.pre_splits = shared_splits(p.row_tiles, stages(shared_len), kSharedMinStages, &p.pre_split_len);
+  }
+  p.own_splits = shared_splits(B, stages((long)max_seq_len - shared_len), 1, &p.own_split_len);
+  return p;
+}
+
+size_t ws_shared(const mla_dims* d, int B, int max_seq_len) {
+  if (B <= 0 || max_seq_len < 1 || max_seq_len > kMaxSeqLen) return 0;
+  const size_t plan = 2 * align256((size_t)B * 4);
+  if (shared_tc_eligible(d)) return shared_tc_layout(d, B, shared_packs(d, B)).bytes;
+  if (decode_mma_eligible(d)) {
+    // every split count is at most these, whatever the prefix's length
+    const long R = (long)B * d->n_heads, sm3 = 3L * device_sm_count();
+    const long stages = ((long)max_seq_len + dmma::kStageTokens - 1) / dmma::kStageTokens;
+    const long pre = std::min(std::max(1L, sm3 / ((R + shared::kRowTile - 1) / shared::kRowTile)), stages);
+    const long own = std::min(std::max(1L, sm3 / B), stages);
+    return plan + align256((size_t)R * (pre + own) * d->d_c * 4) + align256((size_t)R * (pre + own) * 4);
+  }
+  return plan + ws_decode(d, B, max_seq_len);
+}
+
+template <typename T>
+int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_pages, shared::PlanArgs& plan,
+                   void* o_lat, float* lse_out, char* ws, cudaStream_t st, int32_t& launches) {
+  const int B = plan.B, C = decode_clusters(), n_h = d->n_heads;
+  if (!decode_tc_set_smem<T, false, true>()) return MLA_ERR_CUDA;
+  const SharedTcLayout L = shared_tc_layout(d, B, plan.n_shared > 0);
+  plan.prefix_items = L.Mt;
+  plan.first = reinterpret_cast<int*>(ws + L.first);
+  plan.len = reinterpret_cast<int*>(ws + L.len);
+  plan.tile_prefix = reinterpret_cast<int*>(ws + L.tile_prefix);
+  float* o_pre = reinterpret_cast<float*>(ws + L.o_pre);
+  float* o_part = reinterpret_cast<float*>(ws + L.o_part);
+  constexpr bool bf16 = tc::IsBf16<T>::value;
+  constexpr CUtensorMapDataType elem = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  constexpr CUtensorMapDataType f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  tc::SharedTcMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  bool ok = host::encode_pages(&maps.page1, pool, bf16, (uint64_t)num_pages, tc::dec::kD * 2, 1) &&
+            host::encode_pages(&maps.page2, pool, bf16, (uint64_t)num_pages, tc::dec::kD * 2, 2) &&
+            host::encode_pages(&maps.page4, pool, bf16, (uint64_t)num_pages, tc::dec::kD * 2, 4) &&
+            host::encode_chunks(&maps.q9, q, bf16, (uint64_t)B * n_h, tc::dec::kD * 2, 9) &&
+            host::encode_heads_out(&maps.o_part, o_part, f32, 4, (uint64_t)n_h, (uint64_t)B + C) &&
+            host::encode_heads_out32(&maps.o_part_h, o_part, f32, 4, (uint64_t)n_h, (uint64_t)B + C);
+  if (L.Mt > 0)
+    ok = ok && host::encode_heads_out(&maps.o_pre, o_pre, f32, 4, 128, (uint64_t)L.Mt + C) &&
+         host::encode_heads_out32(&maps.o_pre_h, o_pre, f32, 4, 128, (uint64_t)L.Mt + C);
+  else
+    ok = ok && host::encode_heads_out(&maps.o_lat, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B) &&
+         host::encode_heads_out32(&maps.o_lat_h, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B);
+  if (!ok) return MLA_ERR_CUDA;
+  if (launch_pdl(k_shared_plan, dim3(1), dim3(1024), 0, st, plan) != cudaSuccess) return MLA_ERR_CUDA;
+  tc::SharedTcParams p;
+  p.bt = plan.bt;
+  p.max_pages = plan.max_pages;
+  p.seq_lens = plan.len;
+  p.tile_prefix = plan.tile_prefix;
+  p.B = L.Mt + B;
+  p.n_h = n_h;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)(d->d_head + d->d_rope)));
+  p.o_lat = o_lat;
+  p.lse_out = lse_out;
+  p.o_part = o_part;
+  p.lse_part = reinterpret_cast<float*>(ws + L.lse_part);
+  p.f8_pool = nullptr;
+  p.first = plan.first;
+  p.shared_pages = plan.shared_pages;
+  p.prefix_items = L.Mt;
+  p.prefix_len = plan.n_shared * plan.page_size;
+  p.lse_pre = reinterpret_cast<float*>(ws + L.lse_pre);
+  if (launch_pdl(tc::k_decode_tc<T, false, true>, dim3(2 * C), dim3(tc::dec::kThreads), tc::dec::kSmem, st, maps, p) !=
+      cudaSuccess)
+    return MLA_ERR_CUDA;
+  const shared::MergeArgs m{o_pre, p.lse_pre, o_part, p.lse_part, plan.tile_prefix, plan.first, B, n_h, L.Mt, C, o_lat,
+                            lse_out};
+  if (launch_pdl(k_shared_merge<T>, dim3((unsigned)(((long)B * n_h + 7) / 8)), dim3(256), 0, st, m) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  launches += 3;
+  return MLA_OK;
+}
+
+template <typename T>
+bool shared_mma_set_smem() {
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(k_shared_mma<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)dmma::smem_bytes(16 * dmma::kMaxKD)) != cudaSuccess)
+      return false;
+    done[dev].store(true, std::memory_order_release);
+  }
+  return true;
+}
+
+template <typename T>
+int shared_mma_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_pages, shared::PlanArgs& plan,
+                    void* o_lat, float* lse_out, char* ws, cudaStream_t st, int32_t& launches) {
+  const int B = plan.B, D = d->d_c + d->d_rope, shared_len = plan.n_shared * plan.page_size;
+  if (!shared_mma_set_smem<T>()) return MLA_ERR_CUDA;
+  const SharedMmaPlan s = shared_mma_plan(d, B, shared_len, plan.max_seq_len);
+  const int parts = s.pre_splits + s.own_splits;
+  const long R = (long)B * d->n_heads;
+  Carve c{ws};
+  plan.first = c.take<int>((size_t)B);
+  plan.len = c.take<int>((size_t)B);
+  float* o_part = c.take<float>((size_t)R * parts * d->d_c);
+  float* lse_part = c.take<float>((size_t)R * parts);
+  if (launch_pdl(k_shared_plan, dim3(1), dim3(1024), 0, st, plan) != cudaSuccess) return MLA_ERR_CUDA;
+  const float scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)(d->d_head + d->d_rope)));
+  shared::MmaArgs a;
+  a.own = MmaAttnArgs{q, pool, plan.bt, plan.max_pages, plan.len, plan.max_seq_len, (int)num_pages, (int)d->n_heads,
+                      (int)d->d_c, D, (int)d->page_size, scale_log2, s.own_split_len, parts, o_lat, lse_out, o_part,
+                      lse_part, B, plan.first, s.pre_splits};
+  a.shared_pages = plan.shared_pages;
+  a.prefix_len = shared_len;
+  a.row_tiles = s.row_tiles;
+  a.pre_splits = s.pre_splits;
+  a.pre_split_len = s.pre_split_len;
+  a.own_splits = s.own_splits;
+  const long blocks = (long)s.row_tiles * s.pre_splits + (long)B * s.own_splits;
+  if (launch_pdl(k_shared_mma<T>, dim3((unsigned)blocks), dim3(128), dmma::smem_bytes(D), st, a) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  launches += 2;
+  if (parts > 1) {
+    if (launch_pdl(k_lse_merge_warp<T>, dim3((unsigned)((R + 7) / 8)), dim3(256), 0, st,
+                   static_cast<const float*>(o_part), static_cast<const float*>(lse_part), parts, (int)d->d_c, R,
+                   static_cast<T*>(o_lat), lse_out) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    ++launches;
+  }
+  return MLA_OK;
+}
+
+template <typename T>
+int shared_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_pages, const int32_t* bt,
+                int32_t max_pages, const int32_t* seq_lens, int32_t B, int32_t max_seq_len,
+                const int32_t* shared_pages, int32_t num_shared, void* o_lat, float* lse_out, void* ws,
+                cudaStream_t st) {
+  shared::PlanArgs plan{};
+  plan.seq_lens = seq_lens;
+  plan.bt = bt;
+  plan.B = B;
+  plan.max_pages = max_pages;
+  plan.num_pages = num_pages;
+  plan.max_seq_len = max_seq_len;
+  plan.page_size = d->page_size;
+  plan.shared_pages = shared_pages;
+  const bool tc_path = shared_tc_eligible(d), mma_path = decode_mma_eligible(d);
+  plan.n_shared = (tc_path || mma_path) && shared_packs(d, B) ? num_shared : 0;
+  plan.lanes = 1;  // as many threads to a sequence as the block has for B of them
+  while (plan.lanes < 32 && 2 * plan.lanes * B <= 1024) plan.lanes *= 2;
+  int32_t n = 0;
+  int r;
+  if (tc_path) {
+    r = shared_tc_impl<T>(d, q, pool, num_pages, plan, o_lat, lse_out, static_cast<char*>(ws), st, n);
+  } else if (mma_path) {
+    r = shared_mma_impl<T>(d, q, pool, num_pages, plan, o_lat, lse_out, static_cast<char*>(ws), st, n);
+  } else {
+    // no kernel that packs rows for this shape: each sequence over its whole table
+    Carve c{static_cast<char*>(ws)};
+    plan.first = c.take<int>((size_t)B);
+    plan.len = c.take<int>((size_t)B);
+    if (launch_pdl(k_shared_plan, dim3(1), dim3(1024), 0, st, plan) != cudaSuccess) return MLA_ERR_CUDA;
+    ++n;
+    r = decode_impl<T>(d, q, pool, num_pages, bt, max_pages, plan.len, B, max_seq_len, o_lat, lse_out,
+                       static_cast<char*>(ws) + c.off, st, n, false);
+  }
+  if (r != MLA_OK) return r;
+  return finish_launches(MLA_CALL_SHARED_PREFIX_ATTENTION, n);
+}
+
 template <typename T>
 int out_impl(const mla_dims* d, const void* o_lat, const void* w_uv, const void* w_o, void* u, int32_t B, void* ws,
              cudaStream_t st) {
@@ -599,6 +915,7 @@ size_t mla_workspace_size(const mla_dims* dims, int32_t call, int32_t B, int32_t
       return fp8_dims(dims) == MLA_OK && B > 0 && max_seq_len >= 1 && max_seq_len <= kMaxSeqLen
                  ? ws_decode_tc(dims, B)
                  : 0;
+    case MLA_CALL_SHARED_PREFIX_ATTENTION: return ws_shared(dims, B, max_seq_len);
     default: return 0;
   }
 }
@@ -771,6 +1088,71 @@ int mla_prefill_attention(const mla_dims* dims, const void* q, const void* pool,
                               max_seq_len, o_lat, lse_out, ws, st);
 }
 
+int mla_norm_append_kv(const mla_dims* dims, const void* x, int64_t x_stride, const void* gain_c, const void* gain_r,
+                       double eps, const int32_t* seq_idx, const int32_t* pos, const int32_t* block_table,
+                       int32_t num_seqs, int32_t max_pages, void* pool, int32_t num_pages, int32_t T,
+                       mla_stream_t stream) {
+  NvtxRange nvtx_range("mla_norm_append_kv");
+  return norm_append_call<false>(dims, x, x_stride, gain_c, gain_r, eps, seq_idx, pos, block_table, num_seqs, max_pages,
+                                 pool, num_pages, T, stream);
+}
+
+int mla_norm_append_kv_fp8(const mla_dims* dims, const void* x, int64_t x_stride, const void* gain_c,
+                           const void* gain_r, double eps, const int32_t* seq_idx, const int32_t* pos,
+                           const int32_t* block_table, int32_t num_seqs, int32_t max_pages, void* pool,
+                           int32_t num_pages, int32_t T, mla_stream_t stream) {
+  NvtxRange nvtx_range("mla_norm_append_kv_fp8");
+  return norm_append_call<true>(dims, x, x_stride, gain_c, gain_r, eps, seq_idx, pos, block_table, num_seqs, max_pages,
+                                pool, num_pages, T, stream);
+}
+
+int mla_read_kv(const mla_dims* dims, const void* pool, int32_t num_pages, const int32_t* seq_idx, const int32_t* pos,
+                const int32_t* block_table, int32_t num_seqs, int32_t max_pages, void* rows, int64_t rows_stride,
+                int32_t T, mla_stream_t stream) {
+  NvtxRange nvtx_range("mla_read_kv");
+  return read_kv_call<false>(dims, pool, num_pages, seq_idx, pos, block_table, num_seqs, max_pages, rows, rows_stride,
+                             T, stream);
+}
+
+int mla_read_kv_fp8(const mla_dims* dims, const void* pool, int32_t num_pages, const int32_t* seq_idx,
+                    const int32_t* pos, const int32_t* block_table, int32_t num_seqs, int32_t max_pages, void* rows,
+                    int64_t rows_stride, int32_t T, mla_stream_t stream) {
+  NvtxRange nvtx_range("mla_read_kv_fp8");
+  return read_kv_call<true>(dims, pool, num_pages, seq_idx, pos, block_table, num_seqs, max_pages, rows, rows_stride, T,
+                            stream);
+}
+
+int mla_shared_prefix_attention(const mla_dims* dims, const void* q, const void* pool, int32_t num_pages,
+                                const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens, int32_t B,
+                                int32_t max_seq_len, const int32_t* shared_pages, int32_t num_shared_pages,
+                                void* o_lat, float* lse_out, void* ws, size_t ws_bytes, mla_stream_t stream) {
+  NvtxRange nvtx_range("mla_shared_prefix_attention");
+  const int r = check_dims_impl(dims);
+  if (r != MLA_OK) return r;
+  if (B < 0 || B > 65535 || max_seq_len < 1 || max_seq_len > kMaxSeqLen || max_pages <= 0 || num_pages <= 0)
+    return MLA_ERR_INVALID_ARG;
+  if ((long)max_pages * dims->page_size < (long)max_seq_len) return MLA_ERR_INVALID_ARG;
+  if (num_shared_pages < 0 || (long)num_shared_pages * dims->page_size > (long)max_seq_len) return MLA_ERR_INVALID_ARG;
+  // the tiles of the packed rows over the prefix are at most those of B whole sequences, and so are
+  // the sequences' own: twice the pages of B longest sequences stay in int32
+  if (!page_total_fits(dims, 2L * B, max_seq_len)) return MLA_ERR_INVALID_ARG;
+  if (B == 0) {
+    t_launches[MLA_CALL_SHARED_PREFIX_ATTENTION] = 0;
+    return MLA_OK;
+  }
+  if (!q || !pool || !block_table || !seq_lens || !o_lat || !ws) return MLA_ERR_INVALID_ARG;
+  if (num_shared_pages > 0 && !shared_pages) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(pool) || !aligned16(o_lat) || !aligned16(ws) || !aligned16(lse_out))
+    return MLA_ERR_ALIGNMENT;
+  if (ws_bytes < ws_shared(dims, B, max_seq_len)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dims->dtype == MLA_BF16)
+    return shared_impl<__nv_bfloat16>(dims, q, pool, num_pages, block_table, max_pages, seq_lens, B, max_seq_len,
+                                      shared_pages, num_shared_pages, o_lat, lse_out, ws, st);
+  return shared_impl<__half>(dims, q, pool, num_pages, block_table, max_pages, seq_lens, B, max_seq_len, shared_pages,
+                             num_shared_pages, o_lat, lse_out, ws, st);
+}
+
 int mla_out_proj(const mla_dims* dims, const void* o_lat, const void* w_uv, const void* w_o, void* u, int32_t B,
                  void* ws, size_t ws_bytes, mla_stream_t stream) {
   NvtxRange nvtx_range("mla_out_proj");
@@ -854,7 +1236,9 @@ const char* mla_error_string(int code) {
   }
 }
 
-int32_t mla_last_launch_count(int32_t call) { return (call >= 0 && call < 8) ? t_launches[call] : -1; }
+int32_t mla_last_launch_count(int32_t call) {
+  return call >= 0 && call < kNumCalls && call != 8 ? t_launches[call] : -1;  // 8 names no call
+}
 
 int mla_debug_gemm_plan(int32_t M, int32_t N, int32_t K, int32_t batch, int32_t fused_rope, int32_t d_rope,
                         int64_t* out) {
