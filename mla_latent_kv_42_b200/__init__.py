@@ -373,54 +373,84 @@ def out_proj(dims, o_lat, w_uv, w_o, u=None, ws=None, stream=None):
     return u
 
 
-def _args(dims, elem, named):
-    """Checks of the row and shared-prefix calls: each (tensor, name, dtype, shape) lies on the current
-    device, contiguous but for the stride of a two-dimensional row tensor's rows, with that type
-    and shape (None: any size)."""
+# The row and shared-prefix calls are short on the device (3 us for a decode step's rows), so their
+# host side is kept short too: one comparison per tensor decides whether it is as the call needs
+# it, and only a failed one looks closer.
+def _ok(t, dtype, shape, here):
+    return t.dtype is dtype and t.get_device() == here and t.shape == shape and t.is_contiguous()
+
+
+def _refuse(t, name, dtype, shape, here, strided=False):
+    if t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous" + (" but for its rows, a multiple of 8 elements apart" if strided
+                                                     else ""))
+
+
+def _need_all(here, *named):
+    """Each (tensor, name, dtype, shape) lies on the current device, contiguous, with that type and
+    shape."""
+    for t, name, dtype, shape in named:
+        if not _ok(t, dtype, shape, here):
+            _refuse(t, name, dtype, shape, here)
+
+
+def _need_rows(t, name, dtype, shape, here):
+    """The same, but the rows of ``t`` may be strided (a slice of a wider product); their distance."""
+    if _ok(t, dtype, shape, here):
+        return shape[1]
+    if (t.dtype is not dtype or t.get_device() != here or t.shape != shape or t.stride(1) != 1 or t.stride(0) % 8
+            or t.stride(0) < shape[1]):
+        _refuse(t, name, dtype, shape, here, strided=True)
+    return t.stride(0)
+
+
+def _sizes(t, n, name):
+    """Shape of ``t``, which must have n dimensions."""
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _current(stream):
+    """(index of the current device, stream handle)."""
     import torch
     here = torch.cuda.current_device()
-    for t, name, dtype, shape, strided in named:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
-        if t.dtype != (dtype or elem):
-            raise ValueError(f"{name} must be {dtype or elem}, got {t.dtype}")
-        if t.dim() != len(shape) or any(want is not None and want != got for want, got in zip(shape, t.shape)):
-            raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, "
-                             f"got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            # rows with a stride of their own (a slice of a wider product)
-            if not strided or t.stride(1) != 1 or t.stride(0) % 8 or t.stride(0) < t.shape[1]:
-                raise ValueError(f"{name} must be contiguous" +
-                                 (" but for its rows, a multiple of 8 elements apart" if strided else ""))
+    return here, (torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream)
 
 
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0) - t.stride(0) % 8, t.shape[1])
-
-
-def _pool_shape(dims, fp8):
+def _pool_shape(dims, pool, fp8):
     D = dims.d_c + dims.d_rope
-    return (None, dims.page_size * (D + 8)) if fp8 else (None, dims.page_size, D)
+    n = pool.shape[0] if pool.dim() else 0
+    return (n, dims.page_size * (D + 8)) if fp8 else (n, dims.page_size, D)
 
 
 def _norm_append(name, fp8, dims, x, seq_idx, pos, block_table, pool, gain_c, gain_r, eps, stream):
     import torch
     e, i32, D = _elem(dims), torch.int32, dims.d_c + dims.d_rope
-    T = x.shape[0] if x.dim() else 0
-    named = [(x, "x", None, (None, D), True), (seq_idx, "seq_idx", i32, (T,), False), (pos, "pos", i32, (T,), False),
-             (block_table, "block_table", i32, (None, None), False),
-             (pool, "pool", torch.uint8 if fp8 else None, _pool_shape(dims, fp8), False)]
+    here, st = _current(stream)
+    T = _sizes(x, 2, "x")[0]
+    S, width = _sizes(block_table, 2, "block_table")
+    stride = _need_rows(x, "x", e, (T, D), here)
+    shape = _pool_shape(dims, pool, fp8)
+    _need_all(here, (seq_idx, "seq_idx", i32, (T,)), (pos, "pos", i32, (T,)),
+              (block_table, "block_table", i32, (S, width)), (pool, "pool", torch.uint8 if fp8 else e, shape))
     if gain_c is not None:
-        named.append((gain_c, "gain_c", None, (dims.d_c,), False))
+        _need_all(here, (gain_c, "gain_c", e, (dims.d_c,)))
     if gain_r is not None:
-        named.append((gain_r, "gain_r", None, (dims.d_rope,), False))
-    _args(dims, e, named)
+        _need_all(here, (gain_r, "gain_r", e, (dims.d_rope,)))
     cd = c_dims(dims)
-    _check(getattr(_lib(), name)(ctypes.byref(cd), x.data_ptr(), _row_stride(x), _ptr(gain_c), _ptr(gain_r), eps,
-                                 seq_idx.data_ptr(), pos.data_ptr(), block_table.data_ptr(), block_table.shape[0],
-                                 block_table.shape[1], pool.data_ptr(), pool.shape[0], T, _stream(stream)), name)
+    _check(getattr(_lib(), name)(ctypes.byref(cd), x.data_ptr(), stride,
+                                 None if gain_c is None else gain_c.data_ptr(),
+                                 None if gain_r is None else gain_r.data_ptr(), eps, seq_idx.data_ptr(),
+                                 pos.data_ptr(), block_table.data_ptr(), S, width, pool.data_ptr(), shape[0], T, st),
+           name)
     return pool
 
 
@@ -440,16 +470,19 @@ def norm_append_kv_fp8(dims, x, seq_idx, pos, block_table, pool, gain_c=None, ga
 def _read(name, fp8, dims, pool, seq_idx, pos, block_table, out, stream):
     import torch
     e, i32, D = _elem(dims), torch.int32, dims.d_c + dims.d_rope
-    T = seq_idx.shape[0] if seq_idx.dim() else 0
+    here, st = _current(stream)
+    T = _sizes(seq_idx, 1, "seq_idx")[0]
+    S, width = _sizes(block_table, 2, "block_table")
+    shape = _pool_shape(dims, pool, fp8)
+    _need_all(here, (pool, "pool", torch.uint8 if fp8 else e, shape), (seq_idx, "seq_idx", i32, (T,)),
+              (pos, "pos", i32, (T,)), (block_table, "block_table", i32, (S, width)))
     if out is None:
-        out = torch.empty((T, D), dtype=e, device=pool.device)
-    _args(dims, e, [(pool, "pool", torch.uint8 if fp8 else None, _pool_shape(dims, fp8), False),
-                    (seq_idx, "seq_idx", i32, (T,), False), (pos, "pos", i32, (T,), False),
-                    (block_table, "block_table", i32, (None, None), False), (out, "out", None, (T, D), True)])
+        out, stride = pool.new_empty((T, D), dtype=e), D
+    else:
+        stride = _need_rows(out, "out", e, (T, D), here)
     cd = c_dims(dims)
-    _check(getattr(_lib(), name)(ctypes.byref(cd), pool.data_ptr(), pool.shape[0], seq_idx.data_ptr(), pos.data_ptr(),
-                                 block_table.data_ptr(), block_table.shape[0], block_table.shape[1], out.data_ptr(),
-                                 _row_stride(out), T, _stream(stream)), name)
+    _check(getattr(_lib(), name)(ctypes.byref(cd), pool.data_ptr(), shape[0], seq_idx.data_ptr(), pos.data_ptr(),
+                                 block_table.data_ptr(), S, width, out.data_ptr(), stride, T, st), name)
     return out
 
 
@@ -468,26 +501,34 @@ def shared_prefix_attention(dims, q, pool, block_table, seq_lens, max_seq_len, s
     """mla_shared_prefix_attention: decode_attention for a batch whose sequences begin with the pages
     ``shared_pages`` (int32 [num_shared_pages], all full), which are attended once for the batch."""
     import torch
-    e, i32 = _elem(dims), torch.int32
-    B = q.shape[0] if q.dim() else 0
+    e, i32, H = _elem(dims), torch.int32, dims.n_heads
+    here, st = _current(stream)
+    B = _sizes(q, 3, "q")[0]
+    width = _sizes(block_table, 2, "block_table")[1]
+    n_shared = _sizes(shared_pages, 1, "shared_pages")[0]
+    shape = _pool_shape(dims, pool, False)
+    _need_all(here, (q, "q", e, (B, H, dims.d_c + dims.d_rope)), (pool, "pool", e, shape),
+              (block_table, "block_table", i32, (B, width)), (seq_lens, "seq_lens", i32, (B,)),
+              (shared_pages, "shared_pages", i32, (n_shared,)))
     if o_lat is None:
-        o_lat = torch.empty((B, dims.n_heads, dims.d_c), dtype=e, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty((B, dims.n_heads), dtype=torch.float32, device=q.device)
-    named = [(q, "q", None, (None, dims.n_heads, dims.d_c + dims.d_rope), False),
-             (pool, "pool", None, _pool_shape(dims, False), False),
-             (block_table, "block_table", i32, (B, None), False), (seq_lens, "seq_lens", i32, (B,), False),
-             (shared_pages, "shared_pages", i32, (None,), False),
-             (o_lat, "o_lat", None, (B, dims.n_heads, dims.d_c), False)]
+        o_lat = q.new_empty((B, H, dims.d_c))
+    else:
+        _need_all(here, (o_lat, "o_lat", e, (B, H, dims.d_c)))
     if lse is not None:
-        named.append((lse, "lse", torch.float32, (B, dims.n_heads), False))
-    _args(dims, e, named)
-    ws, nbytes = _ws(dims, CALL_SHARED_PREFIX_ATTENTION, B, max_seq_len, ws, q.device)
+        _need_all(here, (lse, "lse", torch.float32, (B, H)))
+    elif want_lse:
+        lse = q.new_empty((B, H), dtype=torch.float32)
     cd = c_dims(dims)
-    _check(_lib().mla_shared_prefix_attention(
-        ctypes.byref(cd), q.data_ptr(), pool.data_ptr(), pool.shape[0], block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), B, int(max_seq_len), shared_pages.data_ptr(), shared_pages.shape[0], o_lat.data_ptr(),
-        _ptr(lse), ws.data_ptr(), nbytes, _stream(stream)), "mla_shared_prefix_attention")
+    lib = _lib()
+    if ws is None:
+        ws = q.new_empty(max(lib.mla_workspace_size(ctypes.byref(cd), CALL_SHARED_PREFIX_ATTENTION, B, max_seq_len),
+                             16), dtype=torch.uint8)
+    elif not ws.is_contiguous() or ws.get_device() != here:
+        raise ValueError(f"ws must be contiguous and on the current device, cuda:{here}")
+    _check(lib.mla_shared_prefix_attention(
+        ctypes.byref(cd), q.data_ptr(), pool.data_ptr(), shape[0], block_table.data_ptr(), width, seq_lens.data_ptr(),
+        B, max_seq_len, shared_pages.data_ptr(), n_shared, o_lat.data_ptr(), None if lse is None else lse.data_ptr(),
+        ws.data_ptr(), ws.nbytes, st), "mla_shared_prefix_attention")
     return o_lat, lse
 
 

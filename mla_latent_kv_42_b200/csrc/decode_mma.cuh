@@ -88,8 +88,8 @@ struct MmaAttnArgs {
 // first 128 threads of the calling CTA (four warps); `sm` holds smem_bytes(D) bytes, 16-aligned.
 // Requirements (checked by the host): n_h <= 16, D % 16 == 0, D <= 192, d_c % 16 == 0, d_c <= 128,
 // page_size % 16 == 0, split_len a multiple of 64. kOwn: the tokens start at first[b], lengths
-// are the plan's (0 for a rejected sequence) and the denominator sums the weights before they are
-// rounded, so that the lse is good to fp32.
+// are the plan's (0 for a rejected sequence) and the lse takes the weights' sum before they are
+// rounded, so that it is good to fp32 (o is divided by the sum of the rounded ones all the same).
 template <typename T, bool kOwn = false>
 __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* sm) {
   using namespace dmma;
@@ -105,7 +105,8 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
   float* __restrict__ o_part = a.o_part;
   float* __restrict__ lse_part = a.lse_part;
   __shared__ int stage_page[kStages][kStageTokens / 16];  // page of each 16-token group of a stage
-  __shared__ float w_ml[kWarps][16][2];                   // per warp and head row: reference max, denominator
+  // per warp and head row: reference max, denominator, and (kOwn) what rounding the weights added
+  __shared__ float w_ml[kWarps][16][kOwn ? 3 : 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, tq = lane & 3;  // mma fragment coordinates
   const int KD = D / 16, ND = d_c / 8;
@@ -183,6 +184,7 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
     for (int e = 0; e < 4; ++e) oacc[j][e] = 0.f;
   float m_ref[2] = {-INFINITY, -INFINITY};  // rows g and g + 8, log2 units
   float lsum[2] = {0.f, 0.f};               // this thread's tokens only (summed over the quad at the end)
+  float ldif[2] = {0.f, 0.f};               // kOwn: sum of the rounded weights less lsum
 
   for (int st = 0; st < kStages - 1; ++st) {
     if (st < n_stages) issue_stage(st);
@@ -223,6 +225,7 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
         if (mx > m_ref[h2] + kLazy) {  // the quad agrees: the same mx and m_ref in its four lanes
           const float alpha = exp2f(m_ref[h2] - mx);
           lsum[h2] *= alpha;
+          if constexpr (kOwn) ldif[h2] *= alpha;
 #pragma unroll
           for (int j = 0; j < kMaxND; ++j) {
             oacc[j][2 * h2] *= alpha;
@@ -237,10 +240,11 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
           v[e] = pe;
         }
         const P2 p01 = Pack<T>::make(v[0], v[1]), p23 = Pack<T>::make(v[2], v[3]);
+        const float2 f01 = Pack<T>::f2(p01), f23 = Pack<T>::f2(p23);
         if constexpr (kOwn) {
           lsum[h2] += (v[0] + v[1]) + (v[2] + v[3]);
+          ldif[h2] += ((f01.x - v[0]) + (f01.y - v[1])) + ((f23.x - v[2]) + (f23.y - v[3]));
         } else {
-          const float2 f01 = Pack<T>::f2(p01), f23 = Pack<T>::f2(p23);
           lsum[h2] += (f01.x + f01.y) + (f23.x + f23.y);
         }
         s[0][2 * h2] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&p01));  // reuse as packed storage
@@ -270,6 +274,10 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
   for (int h2 = 0; h2 < 2; ++h2) {
     lsum[h2] += __shfl_xor_sync(0xffffffffu, lsum[h2], 1);
     lsum[h2] += __shfl_xor_sync(0xffffffffu, lsum[h2], 2);
+    if constexpr (kOwn) {
+      ldif[h2] += __shfl_xor_sync(0xffffffffu, ldif[h2], 1);
+      ldif[h2] += __shfl_xor_sync(0xffffffffu, ldif[h2], 2);
+    }
   }
   __syncthreads();
   float* wo = reinterpret_cast<float*>(sm);  // [warp][16 rows][d_c]
@@ -278,6 +286,10 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
     w_ml[warp][g][1] = lsum[0];
     w_ml[warp][g + 8][0] = m_ref[1];
     w_ml[warp][g + 8][1] = lsum[1];
+    if constexpr (kOwn) {
+      w_ml[warp][g][2] = ldif[0];
+      w_ml[warp][g + 8][2] = ldif[1];
+    }
   }
 #pragma unroll
   for (int j = 0; j < kMaxND; ++j) {
@@ -295,16 +307,17 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
     float m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) m = fmaxf(m, w_ml[w][row][0]);
-    float l = 0.f, acc = 0.f;
+    float l = 0.f, dif = 0.f, acc = 0.f;
     if (m != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = w_ml[w][row][0] == -INFINITY ? 0.f : exp2f(w_ml[w][row][0] - m);
         l = fmaf(f, w_ml[w][row][1], l);
+        if constexpr (kOwn) dif = fmaf(f, w_ml[w][row][2], dif);
         acc = fmaf(f, wo[(w * 16 + row) * d_c + col], acc);
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? 1.f / (l + dif) : 0.f;
     const long bh = (long)b * n_h + row;
     if (n_splits == 1) {
       Out<T>::put(o_lat + bh * d_c + col, acc * inv);

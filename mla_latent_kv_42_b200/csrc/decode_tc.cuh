@@ -140,11 +140,18 @@ struct DecodeTcMaps {
 // result is an fp32 partial.
 struct SharedTcMaps : DecodeTcMaps {
   CUtensorMap o_pre, o_pre_h;  // partials of the prefix items: (512 columns, 128 rows, items + C)
+  CUtensorMap q1;              // queries with boxes of one chunk x own_q_rows rows (own_q_rows > 0)
 };
+// A pair spends on an item, beside its tiles, the time of about kItemUnits more: its queries'
+// load, the pipeline's fill and the epilogue (a one-tile item took 6.7 us where a tile of a long
+// one takes 2.6). With items counted by tiles alone, 256 one-token sequences behind 32768 shared
+// tokens fell to the last pairs and the call took 1520 us.
+constexpr int kItemUnits = 2;
 struct SharedTcParams : DecodeTcParams {
   const int* first;         // [B], -1 for a rejected sequence (which has no tiles)
   const int* shared_pages;  // pages of the prefix
   int prefix_items, prefix_len;
+  int own_q_rows;           // n_h rounded up to 8 where a sequence's rows fit one small box, else 0
   float* lse_pre;           // [items + C][128]
 };
 
@@ -170,29 +177,36 @@ __device__ __forceinline__ ItemIter item_iter(const int* prefix, int B, int clus
   it.b = lo;
   return it;
 }
+// kUnits: places an item takes in the list before its tiles, for its share of the split (kItemUnits
+// below); 0 where the list holds tiles alone.
+template <int kUnits>
 __device__ __forceinline__ bool next_item(ItemIter& it, const int* prefix, Item& out) {
-  if (it.g >= it.g_end) return false;
-  while (prefix[it.b + 1] <= it.g) ++it.b;
-  const int base = prefix[it.b];
-  out.b = it.b;
-  out.n_b = prefix[it.b + 1] - base;
-  out.t0 = (int)(it.g - base);
-  out.t1 = (int)(min(it.g_end, (long)prefix[it.b + 1]) - base);
-  it.g = base + out.t1;
-  return true;
+  while (it.g < it.g_end) {
+    while (prefix[it.b + 1] <= it.g) ++it.b;
+    const int base = prefix[it.b] + kUnits;
+    out.b = it.b;
+    out.n_b = prefix[it.b + 1] - base;
+    out.t0 = max(0, (int)(it.g - base));
+    const long end = min(it.g_end, (long)prefix[it.b + 1]);
+    out.t1 = (int)(end - base);
+    it.g = end;
+    if (kUnits == 0 || out.t1 > out.t0) return true;
+  }
+  return false;
 }
 
 // The pair's tiles in order. Every role walks the same sequence with a cursor of its own:
 // ti counts the pair's tiles, ii its items, t is the tile within sequence item.b (tokens
 // [128t, 128t + 128)).
-struct Cursor {
+template <int kUnits>
+struct CursorOf {
   ItemIter it;
   Item item;
   int t, ti, ii;
   bool valid;
   __device__ __forceinline__ void start(const int* prefix, int B, int cluster, int nclusters) {
     it = item_iter(prefix, B, cluster, nclusters);
-    valid = next_item(it, prefix, item);
+    valid = next_item<kUnits>(it, prefix, item);
     t = valid ? item.t0 : 0;
     ti = 0;
     ii = 0;
@@ -203,7 +217,7 @@ struct Cursor {
     ++ti;
     if (++t == item.t1) {
       ++ii;
-      valid = next_item(it, prefix, item);
+      valid = next_item<kUnits>(it, prefix, item);
       if (valid) t = item.t0;
     }
   }
@@ -271,6 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
                 const std::conditional_t<kShared, SharedTcParams, DecodeTcParams> p) {
   using namespace dec;
   static_assert(!(F8 && kShared), "the shared prefix is read from the element-type cache");
+  using Cursor = CursorOf<kShared ? kItemUnits : 0>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl* ctl = reinterpret_cast<Ctrl*>(data + kDataBytes);
@@ -376,6 +391,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
     else return b * p.n_h;
   };
 
+  auto small_q = [&](int b) {
+    if constexpr (kShared) return b >= p.prefix_items && p.own_q_rows > 0;
+    else return false;
+  };
+
   if (has_work) {
     if (warp == kLoadWarp) {
       // ---------------------------------------------------------------- Q, rope and own-page loads
@@ -409,6 +429,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
             if constexpr (F8) {  // the converting warps turn them into fp16 and publish them
               mbar_arrive_expect_tx(bar(ctl->f8_q), 9 * kChunk);
               tma_load_3d(data_u32 + kQOff, &maps.q9, bar(ctl->f8_q), 0, item_row(b) + 64 * (int)rank, 0);
+            } else if (kShared && small_q(b)) {
+              // few heads: only their rows, and none in rank 1 (the rows left from before are
+              // not stored, and no row of S or O depends on another row)
+              if constexpr (kShared) {
+                const int rows = rank == 0 ? p.own_q_rows : 0;
+                mbar_arrive_expect_tx_cl(lead(ctl->q_full), 9 * 128 * rows);
+                if (rows > 0)
+                  for (int k = 0; k < 9; ++k)
+                    tma_load_3d_pair(data_u32 + kQOff + k * kChunk, &maps.q1, lead(ctl->q_full), 0, item_row(b), k);
+              }
             } else {
               mbar_arrive_expect_tx_cl(lead(ctl->q_full), 9 * kChunk);
               tma_load_3d_pair(data_u32 + kQOff, &maps.q9, lead(ctl->q_full), 0, item_row(b) + 64 * (int)rank, 0);
@@ -807,13 +837,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
       Cursor c;
       c.start(prefix, p.B, cluster, nclusters);
       float m_ref = -INFINITY, lsum = 0.f;
+      float ldif = 0.f;  // kShared: what the rounding of the weights adds to their sum
       int L = 0;
       bool ok = true;
       while (ok && c.valid) {
         const int ti = c.ti, sb = ti & 1, t = c.t;
         if (c.first()) {
           m_ref = -INFINITY;
-          lsum = 0.f;
+          lsum = ldif = 0.f;
           L = item_len(c.item.b);
         }
         if (!wwait(ctl->s_full[sb], (ti >> 1) & 1)) break;
@@ -836,6 +867,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         for (int k = 0; k < 8; ++k) mxs[k] = u2f(sr[k]);
 #pragma unroll
         for (int k = 8; k < 32; ++k) mxs[k & 7] = fmaxf(mxs[k & 7], u2f(sr[k]));
+        // a new item: the other warps' epilogue boxes, which lie in P rows of any warp, have left,
+        // and (kShared) both exchange buffers have been read
+        if (kShared && c.first() && c.ii > 0 && !wwait(ctl->staged, (c.ii - 1) & 1)) break;
         float four[4];
         if (!exchange(fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
                             fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7]))),
@@ -847,12 +881,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         if (mx > m_ref + kLazy) {
           alpha = ex2_approx(m_ref - mx);
           lsum *= alpha;
+          if constexpr (kShared) ldif *= alpha;
           m_ref = mx;
         }
         // the O MMAs of the previous tile are done: P may be overwritten and O rescaled
         if (!wwait(ctl->p_free, (ti & 1) ^ 1)) break;
-        // a new item: the other warps' epilogue boxes, which lie in P rows of any warp, have left
-        if (c.first() && c.ii > 0 && !wwait(ctl->staged, (c.ii - 1) & 1)) break;
+        if (!kShared && c.first() && c.ii > 0 && !wwait(ctl->staged, (c.ii - 1) & 1)) break;
         if (!c.first() && __any_sync(0xffffffffu, alpha != 1.f)) {
           tc_fence_after();
           // two TMEM loads in flight per wait (one with the FP8 cache's smaller register budget)
@@ -874,10 +908,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         }
         // P row h, tokens [32ch, 32ch + 32) of page g: p = 2^(s * scale - m_ref), one FFMA and one
         // ex2 per token. The sum of the rounded weights is the denominator (it matches what the
-        // MMA accumulates); with kShared that of the weights before rounding, so that the lse,
-        // which joins the parts of a sequence, is good to fp32 (rounded weights shift it by up to
-        // 2^-9) and o is off by the weights' own roundings alone.
+        // MMA accumulates). kShared sums the weights before rounding for the lse, which so is good
+        // to fp32 (rounded weights shift it by up to 2^-9), and what rounding adds for the denominator.
         float sums[4] = {0.f, 0.f, 0.f, 0.f};
+        float difs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int u4 = 0; u4 < 4; ++u4) {
           uint32_t w[4];
@@ -887,10 +921,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
             const float w0 = ex2_approx(fmaf(u2f(sr[k]), p.scale_log2, -m_ref));
             const float w1 = ex2_approx(fmaf(u2f(sr[k + 1]), p.scale_log2, -m_ref));
             const typename Pack<PT>::T2 pr2 = Pack<PT>::make(w0, w1);
+            const float2 back = Pack<PT>::f2(pr2);
             if constexpr (kShared) {
               sums[e] += w0 + w1;
+              difs[e] += (back.x - w0) + (back.y - w1);
             } else {
-              const float2 back = Pack<PT>::f2(pr2);
               sums[e] += back.x + back.y;
             }
             w[e] = *reinterpret_cast<const uint32_t*>(&pr2);
@@ -898,6 +933,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
           *reinterpret_cast<uint4*>(p_row_ptr + ((((4 * ch + u4) ^ (h & 7))) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         lsum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        if constexpr (kShared) ldif += (difs[0] + difs[1]) + (difs[2] + difs[3]);
         fence_proxy_async_cta();
         tc_fence_before();
         __syncwarp();
@@ -906,10 +942,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         if (c.last()) {  // ---- epilogue of the item: O / l for this thread's head and columns
           if (!wwait(ctl->p_free, ti & 1)) break;  // the last O MMAs are done
           tc_fence_after();
+          // kShared: the rounding's share of the sum, at most 2^-8 of it, goes along in the bf16
+          // buffer (good to 2^-16 of the sum); that buffer is free too, as above
+          if constexpr (kShared) ctl->xh[ch][lt] = __float2bfloat16_rn(lsum > 0.f ? ldif / lsum : 0.f);
           if (!exchange(lsum, 0, four)) break;
           xnext = 1;
           const float l = (four[0] + four[1]) + (four[2] + four[3]);
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          float denom = l;
+          if constexpr (kShared) {
+            const int l0 = lt & 63;
+            denom = fmaf(four[0], __bfloat162float(ctl->xh[0][l0]), fmaf(four[1], __bfloat162float(ctl->xh[1][l0]),
+                    fmaf(four[2], __bfloat162float(ctl->xh[0][l0 + 64]),
+                         fmaf(four[3], __bfloat162float(ctl->xh[1][l0 + 64]), l))));
+          }
+          const float inv = denom > 0.f ? 1.f / denom : 0.f;
           const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
           const Item& it = c.item;
           bool whole = it.t0 == 0 && it.t1 == it.n_b, packed = false;
@@ -982,7 +1028,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
             }
           };
           // (kShared: a warp none of whose 32 rows are the item's has nothing to store)
-          const int c_end = kShared && head0 >= n_rows ? 0 : 128;
+          int c_end = kShared && head0 >= n_rows ? 0 : 128;
+          if constexpr (kShared) {
+            // Few rows and an fp32 partial: each lane writes its row's 128 columns itself. With
+            // n_rows <= 32 four warps of rank 0 have rows, and the stores queue without a wait,
+            // where the staged rounds wait for the store two rounds back.
+            if (!whole && n_rows <= 32 && c_end > 0) {
+              c_end = 0;
+              float* const dst = p.o_part + (slot * n_rows + h) * kDc + col0;
+#pragma unroll 1
+              for (int c0 = 0; c0 < 128; c0 += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + lane_base + kOCol + 128 * ch + c0, r);
+                tmem_wait_ld();
+                if (h < n_rows) {
+#pragma unroll
+                  for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(dst + c0 + e) =
+                        make_float4(u2f(r[e]) * inv, u2f(r[e + 1]) * inv, u2f(r[e + 2]) * inv, u2f(r[e + 3]) * inv);
+                }
+              }
+            }
+          }
 #pragma unroll 1
           for (int c0 = 0; c0 < c_end; c0 += 32) {
             uint32_t r[32];

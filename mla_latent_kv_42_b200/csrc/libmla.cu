@@ -547,7 +547,7 @@ bool shared_packs(const mla_dims* d, int B) {
 
 struct SharedTcLayout {
   int Mt;  // packed row tiles
-  size_t first, len, tile_prefix, o_pre, lse_pre, o_part, lse_part, bytes;
+  size_t first, len, tile_prefix, pairs, o_pre, lse_pre, o_part, lse_part, bytes;
 };
 SharedTcLayout shared_tc_layout(const mla_dims* d, int B, bool packed) {
   SharedTcLayout L;
@@ -563,6 +563,7 @@ SharedTcLayout shared_tc_layout(const mla_dims* d, int B, bool packed) {
   L.first = take((size_t)B * 4);
   L.len = take((size_t)B * 4);
   L.tile_prefix = take(((size_t)L.Mt + B + 1) * 4);
+  L.pairs = take(((size_t)L.Mt + B) * 4);
   L.o_pre = take(pre_rows * tc::dec::kDc * 4);
   L.lse_pre = take(pre_rows * 4);
   L.o_part = take(own_rows * tc::dec::kDc * 4);
@@ -610,6 +611,10 @@ size_t ws_shared(const mla_dims* d, int B, int max_seq_len) {
   return plan + ws_decode(d, B, max_seq_len);
 }
 
+// Rows up to which the merge gives a row four groups of threads: two row tiles over 74 pairs are cut
+// into 37 parts each, one into 74.
+constexpr unsigned kMergeFewRows = 256;
+
 template <typename T>
 int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_pages, shared::PlanArgs& plan,
                    void* o_lat, float* lse_out, char* ws, cudaStream_t st, int32_t& launches) {
@@ -620,6 +625,8 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   plan.first = reinterpret_cast<int*>(ws + L.first);
   plan.len = reinterpret_cast<int*>(ws + L.len);
   plan.tile_prefix = reinterpret_cast<int*>(ws + L.tile_prefix);
+  plan.pairs = reinterpret_cast<int*>(ws + L.pairs);
+  plan.C = C;
   float* o_pre = reinterpret_cast<float*>(ws + L.o_pre);
   float* o_part = reinterpret_cast<float*>(ws + L.o_part);
   constexpr bool bf16 = tc::IsBf16<T>::value;
@@ -639,6 +646,10 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   else
     ok = ok && host::encode_heads_out(&maps.o_lat, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B) &&
          host::encode_heads_out32(&maps.o_lat_h, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B);
+  // a sequence's own item of at most 32 heads loads its own query rows, 8 at least, chunk by chunk
+  const int own_q_rows = L.Mt > 0 && n_h <= 32 ? (n_h + 7) / 8 * 8 : 0;
+  if (own_q_rows > 0)
+    ok = ok && host::encode_chunks(&maps.q1, q, bf16, (uint64_t)B * n_h, tc::dec::kD * 2, 1, (uint32_t)own_q_rows);
   if (!ok) return MLA_ERR_CUDA;
   if (launch_pdl(k_shared_plan, dim3(1), dim3(1024), 0, st, plan) != cudaSuccess) return MLA_ERR_CUDA;
   tc::SharedTcParams p;
@@ -658,14 +669,18 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   p.shared_pages = plan.shared_pages;
   p.prefix_items = L.Mt;
   p.prefix_len = plan.n_shared * plan.page_size;
+  p.own_q_rows = own_q_rows;
   p.lse_pre = reinterpret_cast<float*>(ws + L.lse_pre);
   if (launch_pdl(tc::k_decode_tc<T, false, true>, dim3(2 * C), dim3(tc::dec::kThreads), tc::dec::kSmem, st, maps, p) !=
       cudaSuccess)
     return MLA_ERR_CUDA;
-  const shared::MergeArgs m{o_pre, p.lse_pre, o_part, p.lse_part, plan.tile_prefix, plan.first, B, n_h, L.Mt, C, o_lat,
-                            lse_out};
-  if (launch_pdl(k_shared_merge<T>, dim3((unsigned)(((long)B * n_h + 7) / 8)), dim3(256), 0, st, m) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  const shared::MergeArgs m{o_pre, p.lse_pre, o_part, p.lse_part, plan.tile_prefix, plan.pairs, plan.first, B, n_h,
+                            L.Mt, C, o_lat, lse_out};
+  const unsigned R = (unsigned)((long)B * n_h);
+  const cudaError_t e = R <= kMergeFewRows ? launch_pdl(k_shared_merge<T, 128, 4>, dim3(R), dim3(512), 0, st, m)
+                                           : launch_pdl(k_shared_merge<T, 64, 1>, dim3((R + shared::kMergeRows - 1) / shared::kMergeRows),
+                                                        dim3(64 * shared::kMergeRows), 0, st, m);
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
   launches += 3;
   return MLA_OK;
 }
@@ -1133,9 +1148,9 @@ int mla_shared_prefix_attention(const mla_dims* dims, const void* q, const void*
     return MLA_ERR_INVALID_ARG;
   if ((long)max_pages * dims->page_size < (long)max_seq_len) return MLA_ERR_INVALID_ARG;
   if (num_shared_pages < 0 || (long)num_shared_pages * dims->page_size > (long)max_seq_len) return MLA_ERR_INVALID_ARG;
-  // the tiles of the packed rows over the prefix are at most those of B whole sequences, and so are
-  // the sequences' own: twice the pages of B longest sequences stay in int32
-  if (!page_total_fits(dims, 2L * B, max_seq_len)) return MLA_ERR_INVALID_ARG;
+  // the places of all items in the attention kernel's list stay in int32: a packed row tile and a
+  // sequence take at most two more than the pages of a longest sequence
+  if (2L * B * (pages_of(dims, max_seq_len) + tc::kItemUnits) > (long)INT32_MAX) return MLA_ERR_INVALID_ARG;
   if (B == 0) {
     t_launches[MLA_CALL_SHARED_PREFIX_ATTENTION] = 0;
     return MLA_OK;

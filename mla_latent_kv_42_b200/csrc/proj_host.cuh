@@ -81,14 +81,15 @@ inline bool encode_2d(CUtensorMap* map, const void* base, bool bf16, uint64_t in
 
 // 3-D view of a row-major [rows][9 * 64] tensor of 16-bit elements, rows `row_bytes` apart, as
 // (64 columns, rows, 9 column chunks): one box of (64, 64, depth) lands in shared memory as
-// `depth` consecutive 64 x 64 chunks, each in the 128-byte-swizzled layout of a 2-D 64 x 64 box.
+// `depth` consecutive 64 x 64 chunks, each in the 128-byte-swizzled layout of a 2-D 64 x 64 box
+// (box_rows: fewer rows, a multiple of 8).
 inline bool encode_chunks(CUtensorMap* map, const void* base, bool bf16, uint64_t rows, uint64_t row_bytes,
-                          uint32_t depth) {
+                          uint32_t depth, uint32_t box_rows = 64) {
   auto fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {64, rows, 9};
   cuuint64_t strides[2] = {row_bytes, 128};
-  cuuint32_t box[3] = {64, 64, depth};
+  cuuint32_t box[3] = {64, box_rows, depth};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

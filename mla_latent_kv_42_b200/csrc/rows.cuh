@@ -16,7 +16,8 @@
 namespace mla {
 namespace rows {
 constexpr int kGroups = 3;    // 8-element groups per lane: D <= 768
-constexpr int kPowers = 9;    // d_rope / 2 <= 284 < 2^9
+constexpr int kMaxPairs = 284;  // d_rope / 2
+constexpr int kPowers = 9;      // kMaxPairs < 2^9
 constexpr int kWarps = 8;     // per CTA
 constexpr int kReadTokens = 4;  // tokens a warp of k_read_rows has in flight
 
@@ -59,6 +60,14 @@ __device__ __forceinline__ void turn_cos_sin(int pos, double turns, float& c, fl
   sincospif(2.f * (float)(t - rint(t)), &s, &c);
 }
 
+// v / s for a normal s with a normal reciprocal, given inv = 1 / s rounded: the quotient's remainder is
+// exact in an fma, and one step with it gives the correctly rounded quotient (Markstein 1990,
+// theorem on division from a correctly rounded reciprocal). Three instructions to the value.
+__device__ __forceinline__ float quotient(float v, float s, float inv) {
+  const float q = v * inv;
+  return fmaf(fmaf(-q, s, v), inv, q);
+}
+
 struct AppendArgs {
   const void* x;  // [T] rows of D elements, x_stride apart
   long x_stride;
@@ -74,51 +83,57 @@ struct AppendArgs {
 };
 }  // namespace rows
 
+// A warp per token, the next token's row, position and sequence requested before this one's
+// arithmetic. The frequencies are formed once per CTA in shared memory (they are doubles), and the
+// warp's lanes share a token's cosines and sines, one pair each, through it.
 template <typename T, bool kFp8>
 __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::AppendArgs a) {
   using namespace rows;
   using P2 = typename Pack<T>::T2;
-  const int lane = threadIdx.x & 31;
+  __shared__ double s_turns[kMaxPairs];
+  __shared__ float2 s_cs[kWarps][kMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.D / 8, Gc = a.d_c / 8;  // groups of the row, of its latent part
+  const int pairs = (a.D - a.d_c) / 2;
+  if (a.turns.table == nullptr)  // from the arguments alone: ahead of the wait
+    for (int k = threadIdx.x; k < pairs; k += 32 * kWarps) s_turns[k] = a.turns(k);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
-  // this lane's groups are the same for every token: their gains and frequencies stay in registers
-  uint4 gain[kGroups];
-  double turns[kGroups][4];
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const int g = lane + 32 * i;
-    gain[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) turns[i][e] = 0.0;
-    if (g < Gc) {
-      if (a.g_c != nullptr) gain[i] = ldg16(static_cast<const T*>(a.g_c) + 8 * g);
-    } else if (g < G) {
-      if (a.g_r != nullptr) gain[i] = ldg16(static_cast<const T*>(a.g_r) + 8 * (g - Gc));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) turns[i][e] = a.turns(4 * (g - Gc) + e);
-    }
-  }
+  if (a.turns.table != nullptr)
+    for (int k = threadIdx.x; k < pairs; k += 32 * kWarps) s_turns[k] = a.turns(k);
+  __syncthreads();
+  float2* const cs = s_cs[warp];
   const int n_warps = gridDim.x * kWarps;
-  for (int t = blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += n_warps) {
-    const T* src = static_cast<const T*>(a.x) + (long)t * a.x_stride;
-    uint4 raw[kGroups];
+  int t = blockIdx.x * kWarps + warp;
+  uint4 raw[kGroups];
+  int p = 0, seq = 0;
+  auto request = [&](int tt) {
+    if (tt >= a.T) return;
+    const T* src = static_cast<const T*>(a.x) + (long)tt * a.x_stride;
+    p = a.pos[tt];
+    seq = a.seq_idx[tt];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       const int g = lane + 32 * i;
       raw[i] = g < G ? *reinterpret_cast<const uint4*>(src + 8 * g) : make_uint4(0, 0, 0, 0);
     }
-    const int p = a.pos[t];
-    const long slot = a.slot(a.seq_idx[t], p);
+  };
+  request(t);
+  for (; t < a.T; t += n_warps) {
+    const int pos = p;
+    const long slot = a.slot(seq, pos);
+    float v[kGroups][8];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) unpack8<T>(raw[i], v[i]);
+    request(t + n_warps);
     if (slot < 0) {
       if (lane == 0) record_error(MLA_ERR_BAD_PAGE);
       continue;
     }
-    float v[kGroups][8];
+    for (int k = lane; k < pairs; k += 32) turn_cos_sin(pos, s_turns[k], cs[k].x, cs[k].y);
     float ss_c = 0.f, ss_r = 0.f;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-      unpack8<T>(raw[i], v[i]);
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
@@ -127,14 +142,16 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
     }
     if (a.g_c != nullptr) ss_c = rsqrtf(warp_sum(ss_c) / (float)a.d_c + a.eps);
     if (a.g_r != nullptr) ss_r = rsqrtf(warp_sum(ss_r) / (float)(a.D - a.d_c) + a.eps);
+    __syncwarp();  // cs is written
     float mc = 0.f, mr = 0.f;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       const int g = lane + 32 * i;
       const bool lat = g < Gc;
-      if ((lat ? a.g_c : a.g_r) != nullptr) {
+      const void* gain = lat ? a.g_c : a.g_r;
+      if (gain != nullptr && g < G) {
         float gf[8];
-        unpack8<T>(gain[i], gf);
+        unpack8<T>(ldg16(static_cast<const T*>(gain) + 8 * (lat ? g : g - Gc)), gf);
         const float rs = lat ? ss_c : ss_r;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * rs * gf[e];
@@ -142,11 +159,10 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
       if (!lat && g < G) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float c, s;
-          turn_cos_sin(p, turns[i][e], c, s);
+          const float2 c = cs[4 * (g - Gc) + e];
           const float x0 = v[i][2 * e], x1 = v[i][2 * e + 1];
-          v[i][2 * e] = x0 * c - x1 * s;
-          v[i][2 * e + 1] = x0 * s + x1 * c;
+          v[i][2 * e] = x0 * c.x - x1 * c.y;
+          v[i][2 * e + 1] = x0 * c.y + x1 * c.x;
         }
       }
       if constexpr (kFp8) {
@@ -154,9 +170,10 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[i][e]));
         if (lat) mc = fmaxf(mc, m);
-        else if (g < G) mr = fmaxf(mr, m);
+        else mr = fmaxf(mr, m);
       }
     }
+    __syncwarp();  // cs has been read
     if constexpr (!kFp8) {
       T* dst = static_cast<T*>(a.pool) + slot * a.D;
 #pragma unroll
@@ -178,27 +195,35 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
       mr = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mr)));
       const float sc = mc > 0.f ? mc / fp8::kE4m3Max : 1.f;
       const float sr = mr > 0.f ? mr / fp8::kE4m3Max : 1.f;
+      const float ic = 1.f / sc, ir = 1.f / sr;
+      // scales whose reciprocal or whose products with values are not normal divide as they are
+      const bool plain = !(fminf(sc, sr) > 0x1p-100f && fmaxf(sc, sr) < 0x1p100f);
       const int ps = a.slot.page_size;
       const long page = slot / ps;
       const int row = (int)(slot - page * ps);
       uint8_t* const pg = static_cast<uint8_t*>(a.pool) + page * fp8::page_bytes(ps, a.D);
+      auto store = [&](auto divide) {
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int g = lane + 32 * i;
-        if (g < G) {
-          const float sg = g < Gc ? sc : sr;
-          uint32_t q[2];
+        for (int i = 0; i < kGroups; ++i) {
+          const int g = lane + 32 * i;
+          if (g < G) {
+            const float s = g < Gc ? sc : sr, inv = g < Gc ? ic : ir;
+            uint32_t q[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-                make_float2(v[i][4 * h] / sg, v[i][4 * h + 1] / sg), __NV_SATFINITE, __NV_E4M3);
-            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-                make_float2(v[i][4 * h + 2] / sg, v[i][4 * h + 3] / sg), __NV_SATFINITE, __NV_E4M3);
-            q[h] = (uint32_t)lo | ((uint32_t)hi << 16);
+            for (int h = 0; h < 2; ++h) {
+              const float* x = v[i] + 4 * h;
+              const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+                  make_float2(divide(x[0], s, inv), divide(x[1], s, inv)), __NV_SATFINITE, __NV_E4M3);
+              const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+                  make_float2(divide(x[2], s, inv), divide(x[3], s, inv)), __NV_SATFINITE, __NV_E4M3);
+              q[h] = (uint32_t)lo | ((uint32_t)hi << 16);
+            }
+            *reinterpret_cast<uint2*>(pg + (long)row * a.D + 8 * g) = make_uint2(q[0], q[1]);
           }
-          *reinterpret_cast<uint2*>(pg + (long)row * a.D + 8 * g) = make_uint2(q[0], q[1]);
         }
-      }
+      };
+      if (plain) store([](float x, float s, float) { return x / s; });
+      else store([](float x, float s, float inv) { return quotient(x, s, inv); });
       if (lane == 0) *reinterpret_cast<float2*>(pg + (long)ps * a.D + 8 * row) = make_float2(sc, sr);
     }
   }

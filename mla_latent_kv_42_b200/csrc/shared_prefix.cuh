@@ -28,7 +28,10 @@ struct PlanArgs {
   int prefix_items;  // packed row tiles
   int* first;        // [B] first token of the sequence's own part, -1 for a rejected sequence
   int* len;          // [B] its length, 0 for a rejected sequence
-  int* tile_prefix;  // [prefix_items + B + 1] 128-token tiles before each item, or null
+  int* tile_prefix;  // [prefix_items + B + 1] places before each item in the list of the items'
+                     // tiles, kItemUnits places and then its tiles to an item that has any; or null
+  int* pairs;        // [prefix_items + B] first and last pair of an item's tiles, c0 | c1 << 16, -1: none
+  int C;             // pairs
 };
 }  // namespace shared
 
@@ -44,19 +47,22 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
   if (threadIdx.x == 0) griddep_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = a.page_size, shared_len = a.n_shared * P;
+  // the first sequence's length is requested beside the shared pages
+  const int per_pass = 1024 / a.lanes, sub = tid & (a.lanes - 1);
+  const int b_first = tid / a.lanes;
+  const int L_first = b_first < a.B ? a.seq_lens[b_first] : 0;
   bool bad = false;
   for (int t = tid; t < a.n_shared; t += 1024) {
     const int pg = a.shared_pages[t];
     bad |= pg < 0 || pg >= a.num_pages;
   }
   const bool bad_prefix = __syncthreads_or(bad);
-  const int per_pass = 1024 / a.lanes, sub = tid & (a.lanes - 1);
   for (int b0 = 0; b0 < a.B; b0 += per_pass) {
-    const int b = b0 + tid / a.lanes;
+    const int b = b0 + b_first;
     int L = 0, n = 0, f = 0;
     bool len_ok = false;
     if (b < a.B) {
-      L = a.seq_lens[b];
+      L = b0 == 0 ? L_first : a.seq_lens[b];
       len_ok = L >= 1 && L <= a.max_seq_len;
       n = len_ok ? (L + P - 1) / P : 0;
       len_ok = len_ok && n <= a.max_pages;
@@ -80,14 +86,14 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
       a.first[b] = ok ? f : -1;
       a.len[b] = ok ? L : 0;
       if (a.tile_prefix != nullptr) {
-        const int tiles = ok ? (int)(((long)(L - f) + tc::dec::kTile - 1) / tc::dec::kTile) : 0;
+        const int tiles = ok && L > f ? tc::kItemUnits + (L - f + tc::dec::kTile - 1) / tc::dec::kTile : 0;
         if (a.B <= shared::kScanSeqs) s_count[b] = tiles;
         else a.tile_prefix[a.prefix_items + b] = tiles;
       }
     }
   }
   if (a.tile_prefix == nullptr) return;
-  const int nt = bad_prefix ? 0 : (shared_len + tc::dec::kTile - 1) / tc::dec::kTile;
+  const int nt = bad_prefix || shared_len == 0 ? 0 : tc::kItemUnits + (shared_len + tc::dec::kTile - 1) / tc::dec::kTile;
   int* const mine = a.tile_prefix + a.prefix_items;
   for (int i = tid; i < a.prefix_items; i += 1024) a.tile_prefix[i] = i * nt;
   __syncthreads();
@@ -115,13 +121,24 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
     warp_total[lane] = w;
   }
   __syncthreads();
+  const long T = (long)a.prefix_items * nt + warp_total[31];
+  const bool narrow = T < (1u << 31) / tc::kMaxDecodeClusters;  // a pair's number fits 32-bit arithmetic
+  auto pair_of = [&](int g) {
+    return narrow ? (int)(((unsigned)(g + 1) * (unsigned)a.C - 1u) / (unsigned)T) : tc::cluster_of(g, T, a.C);
+  };
+  auto pairs_of = [&](int begin, int n) {
+    if (n == 0) return -1;
+    return pair_of(begin + tc::kItemUnits) | (pair_of(begin + n - 1) << 16);
+  };
+  for (int i = tid; i < a.prefix_items; i += 1024) a.pairs[i] = pairs_of(i * nt, nt);
   int run = a.prefix_items * nt + incl - sum + (warp > 0 ? warp_total[warp - 1] : 0);
   for (int b = b0; b < b1; ++b) {
     const int n = count[b];  // read before the same place may be overwritten
     mine[b] = run;
+    a.pairs[a.prefix_items + b] = pairs_of(run, n);
     run += n;
   }
-  if (tid == 1023) mine[a.B] = a.prefix_items * nt + warp_total[31];
+  if (tid == 1023) mine[a.B] = (int)T;
 }
 
 namespace shared {
@@ -129,117 +146,173 @@ struct MergeArgs {
   const float *o_pre, *lse_pre;    // prefix partials: slots of 128 packed rows
   const float *o_part, *lse_part;  // own partials: slots of n_h rows
   const int* tile_prefix;
+  const int* pairs;
   const int* first;
   int B, n_h, prefix_items, C;
   void* o_lat;
   float* lse_out;
 };
-// Partial slots of an item whose tiles start at g0: part k is in slot item + pair, the pair being
-// c0 + k when every pair has tiles (T >= C), else the one that owns tile g0 + k (no two tiles
-// share a pair then).
+// Partial slots of an item: part k is in slot `item` + its pair. When every pair has places in the
+// list (T >= C) the pairs between the first and the last one of the item's tiles lie within them, so
+// the slots are consecutive; else part k is tile k, alone on the pair that has its place.
 struct Parts {
-  long T;
-  int C, item, g0, c0, n;
-  __device__ __forceinline__ Parts(long T_, int C_, int item_, int g0_, int g1) : T(T_), C(C_), item(item_), g0(g0_) {
-    c0 = 0;
-    n = 0;
-    if (g1 <= g0) return;
-    c0 = tc::cluster_of(g0, T, C);
-    n = T >= C ? tc::cluster_of(g1 - 1, T, C) - c0 + 1 : g1 - g0;
+  int first, n, item, g0;
+  __device__ __forceinline__ Parts(bool dense, int item_, const int* prefix, int pairs)
+      : first(item_ + (pairs & 0xffff)), n(0), item(item_), g0(0) {
+    if (pairs < 0) return;
+    n = (pairs >> 16) - (pairs & 0xffff) + 1;
+    if (!dense) {
+      g0 = prefix[0] + tc::kItemUnits;
+      n = prefix[1] - g0;
+    }
   }
-  __device__ __forceinline__ int slot(int k) const {
-    return item + (T >= C ? c0 + k : tc::cluster_of(g0 + k, T, C));
+  template <bool kDense>
+  __device__ __forceinline__ int slot(int k, int T, int C) const {
+    return kDense ? first + k : item + ((g0 + k + 1) * C - 1) / T;
   }
 };
+constexpr int kMergeAhead = 8;  // parts a thread has in flight (four where it has two vectors of each)
+constexpr int kMergeRows = 4;   // rows of a block whose rows have one group each
 }  // namespace shared
 
-// Joins each query row's partials, those over the prefix and those over its own tokens, in pair
-// order. A warp per row, each lane 16 of the 512 latent values; two parts' loads in flight. A
-// rejected sequence gets zeros and an lse of -inf. Without prefix items a row that one pair
-// finished is already in o_lat. Bound by the 2 KB of a partial row: R rows with n parts move
-// 2048 R n bytes.
-template <typename T>
-__global__ void __launch_bounds__(256) k_shared_merge(const shared::MergeArgs a) {
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch();
-  const int lane = threadIdx.x & 31;
-  const int r = (int)(blockIdx.x * 8 + (threadIdx.x >> 5));
-  if (r >= a.B * a.n_h) return;
-  const int b = r / a.n_h, h = r - b * a.n_h;
-  const int f = a.first[b];
-  const long T_ = a.tile_prefix[a.prefix_items + a.B];
-  T* const out = static_cast<T*>(a.o_lat) + (long)r * tc::dec::kDc;
-  if (f < 0) {
-    for (int e = lane; e < tc::dec::kDc / 8; e += 32) *reinterpret_cast<uint4*>(out + 8 * e) = make_uint4(0, 0, 0, 0);
-    if (a.lse_out != nullptr && lane == 0) a.lse_out[r] = -INFINITY;
-    return;
-  }
-  const int it = r >> 7;  // the packed tile of this row
-  const bool pre = a.prefix_items > 0 && f > 0;
-  const shared::Parts pp(T_, a.C, it, pre ? a.tile_prefix[it] : 0, pre ? a.tile_prefix[it + 1] : 0);
-  const shared::Parts po(T_, a.C, b, a.tile_prefix[a.prefix_items + b], a.tile_prefix[a.prefix_items + b + 1]);
-  if (a.prefix_items == 0 && po.n == 1) return;
-  const int n = pp.n + po.n;
+// Joins each query row's partials, those over the prefix and those over its own tokens, in a fixed
+// order. kGroups groups of kLanes threads share a row and take its parts in turn, a thread 512 /
+// kLanes of the latent values and kMergeAhead parts in flight: four groups where the rows are few
+// and so are cut into many parts, one of fewer threads where they are many (at 8192 rows of two
+// parts the instructions of 128 threads a row took longer than the partials' bytes). Every warp
+// forms the weights of up to 32 parts for itself; more go through shared memory where a block has one
+// row. A rejected sequence gets zeros and an lse of -inf. Without prefix items a row that one pair
+// finished is already in o_lat. A block of four groups has one row, else kMergeRows of them.
+template <typename T, int kLanes, int kGroups, bool kDense>
+__device__ __forceinline__ void merge_row(const shared::MergeArgs& a, const shared::Parts& pp, const shared::Parts& po,
+                                          int r, int b, int T_) {
+  constexpr int kVec = 128 / kLanes, kThreads = kLanes * kGroups, kWarps = kThreads / 32;
+  constexpr int kMergeAhead = shared::kMergeAhead / kVec;
+  __shared__ float s_w[2 * tc::kMaxDecodeClusters];
+  __shared__ float s_red[kWarps];
+  __shared__ float4 s_acc[kGroups > 1 ? kGroups - 1 : 1][kGroups > 1 ? 128 : 1];
+  const int tid = threadIdx.x % kThreads, lane = tid & 31, warp = tid >> 5, group = tid / kLanes;
+  const int col = 4 * (tid % kLanes);
+  const int n = pp.n + po.n, h = r - b * a.n_h;
   auto row_of = [&](int k) -> long {  // row of part k among the rows of its buffer
-    return k < pp.n ? (long)pp.slot(k) * 128 + (r & 127) : (long)po.slot(k - pp.n) * a.n_h + h;
+    return k < pp.n ? (long)pp.template slot<kDense>(k, T_, a.C) * 128 + (r & 127)
+                    : (long)po.template slot<kDense>(k - pp.n, T_, a.C) * a.n_h + h;
   };
-  auto lse_of = [&](int k) { return k < pp.n ? a.lse_pre[row_of(k)] : a.lse_part[row_of(k)]; };
-  auto load = [&](int k, float4 (&v)[4]) {
-    const float4* src = reinterpret_cast<const float4*>((k < pp.n ? a.o_pre : a.o_part) + row_of(k) * tc::dec::kDc);
+  auto lse_of = [&](int k) { return (k < pp.n ? a.lse_pre : a.lse_part)[row_of(k)]; };
+  float4 v[kMergeAhead][kVec];
+  auto load = [&](int k, float4 (&x)[kVec]) {
+    if (k >= n) return;
+    const float* src = (k < pp.n ? a.o_pre : a.o_part) + row_of(k) * tc::dec::kDc + col;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = src[lane + 32 * j];
+    for (int j = 0; j < kVec; ++j) x[j] = *reinterpret_cast<const float4*>(src + 4 * kLanes * j);
   };
-  // the first two parts are requested before the weights are formed
-  float4 v0[4], v1[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v0[j] = v1[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (n > 0) load(0, v0);
-  if (n > 1) load(1, v1);
+  for (int u = 0; u < kMergeAhead; ++u) load(group + kGroups * u, v[u]);  // requested before the weights are formed
+  auto warp_max = [](float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  };
+  const bool many = kGroups > 1 && n > 32;  // the same in the whole block
+  float mx = -INFINITY;
   const float mine = lane < n ? lse_of(lane) : -INFINITY;
-  float mx = mine;
-  for (int k = lane + 32; k < n; k += 32) mx = fmaxf(mx, lse_of(k));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (!many) {
+    mx = mine;
+    for (int k = lane + 32; k < n; k += 32) mx = fmaxf(mx, lse_of(k));
+    mx = warp_max(mx);
+  } else {
+    for (int k = tid; k < n; k += kThreads) mx = fmaxf(mx, s_w[k] = lse_of(k));
+    mx = warp_max(mx);
+    if (lane == 0) s_red[warp] = mx;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_red[w]);
+  }
   auto weight_of = [&](float l) { return l > -INFINITY ? exp2f((l - mx) * kLog2e) : 0.f; };
-  float z = weight_of(mine);
-  for (int k = lane + 32; k < n; k += 32) z += weight_of(lse_of(k));
+  const float w_lane = weight_of(mine);
+  float z = 0.f;
+  if (!many) {
+    z = w_lane;
+    for (int k = lane + 32; k < n; k += 32) z += weight_of(lse_of(k));
+    z = warp_sum(z);
+  } else {
+    __syncthreads();  // s_red has been read
+    for (int k = tid; k < n; k += kThreads) z += s_w[k] = weight_of(s_w[k]);
+    z = warp_sum(z);
+    if (lane == 0) s_red[warp] = z;
+    __syncthreads();
+    z = 0.f;
+    for (int w = 0; w < kWarps; ++w) z += s_red[w];
+  }
+  float4 acc[kVec];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  float4 acc[4];
+  for (int j = 0; j < kVec; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = group; k0 < n; k0 += kGroups * kMergeAhead) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](int k, const float4 (&v)[4]) {
-    const float l = k < 32 ? __shfl_sync(0xffffffffu, mine, k) : lse_of(k);
-    const float w = weight_of(l);
+    for (int u = 0; u < kMergeAhead; ++u) {
+      const int k = k0 + kGroups * u;
+      if (k >= n) break;  // the same in the whole warp
+      const float w = many ? s_w[k] : k < 32 ? __shfl_sync(0xffffffffu, w_lane, k) : weight_of(lse_of(k));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      acc[j].x = fmaf(w, v[j].x, acc[j].x);
-      acc[j].y = fmaf(w, v[j].y, acc[j].y);
-      acc[j].z = fmaf(w, v[j].z, acc[j].z);
-      acc[j].w = fmaf(w, v[j].w, acc[j].w);
+      for (int j = 0; j < kVec; ++j) {
+        acc[j].x = fmaf(w, v[u][j].x, acc[j].x);
+        acc[j].y = fmaf(w, v[u][j].y, acc[j].y);
+        acc[j].z = fmaf(w, v[u][j].z, acc[j].z);
+        acc[j].w = fmaf(w, v[u][j].w, acc[j].w);
+      }
+      load(k + kGroups * kMergeAhead, v[u]);
     }
-  };
-  for (int k = 0; k < n; k += 2) {
-    float4 n0[4], n1[4];
-    if (k + 2 < n) load(k + 2, n0);
-    if (k + 3 < n) load(k + 3, n1);
-    add(k, v0);
-    if (k + 1 < n) add(k + 1, v1);
+  }
+  if constexpr (kGroups > 1) {
+    static_assert(kVec == 1, "one vector per thread where groups are joined");
+    if (group > 0) s_acc[group - 1][tid % kLanes] = acc[0];
+    __syncthreads();
+    if (group > 0) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v0[j] = n0[j];
-      v1[j] = n1[j];
+    for (int g = 0; g < kGroups - 1; ++g) {
+      const float4 o = s_acc[g][tid];
+      acc[0].x += o.x;
+      acc[0].y += o.y;
+      acc[0].z += o.z;
+      acc[0].w += o.w;
     }
   }
   const float inv = z > 0.f ? 1.f / z : 0.f;
-  typename Pack<T>::T2* dst = reinterpret_cast<typename Pack<T>::T2*>(out);
+  T* const out = static_cast<T*>(a.o_lat) + (long)r * tc::dec::kDc + col;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int e = 2 * (lane + 32 * j);
-    dst[e] = Pack<T>::make(acc[j].x * inv, acc[j].y * inv);
-    dst[e + 1] = Pack<T>::make(acc[j].z * inv, acc[j].w * inv);
+  for (int j = 0; j < kVec; ++j) {
+    const typename Pack<T>::T2 two[2] = {Pack<T>::make(acc[j].x * inv, acc[j].y * inv),
+                                         Pack<T>::make(acc[j].z * inv, acc[j].w * inv)};
+    *reinterpret_cast<uint2*>(out + 4 * kLanes * j) = *reinterpret_cast<const uint2*>(two);
   }
-  if (a.lse_out != nullptr && lane == 0) a.lse_out[r] = z > 0.f ? mx + logf(z) : -INFINITY;
+  if (a.lse_out != nullptr && tid == 0) a.lse_out[r] = z > 0.f ? mx + logf(z) : -INFINITY;
+}
+
+template <typename T, int kLanes, int kGroups>
+__global__ void __launch_bounds__(kLanes* kGroups * (kGroups > 1 ? 1 : shared::kMergeRows))
+    k_shared_merge(const shared::MergeArgs a) {
+  constexpr int kThreads = kLanes * kGroups, kRows = kGroups > 1 ? 1 : shared::kMergeRows;
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch();
+  const int r = (int)blockIdx.x * kRows + (int)threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
+  if (r >= a.B * a.n_h) return;
+  const int b = r / a.n_h;
+  const int it = r >> 7;  // the packed tile of this row
+  const int f = a.first[b], T_ = a.tile_prefix[a.prefix_items + a.B];
+  const int po_pairs = a.pairs[a.prefix_items + b];
+  const int pp_pairs = a.prefix_items > 0 && f > 0 ? a.pairs[it] : -1;
+  if (f < 0) {
+    T* const out = static_cast<T*>(a.o_lat) + (long)r * tc::dec::kDc;
+    for (int e = tid; e < tc::dec::kDc / 8; e += kThreads)
+      *reinterpret_cast<uint4*>(out + 8 * e) = make_uint4(0, 0, 0, 0);
+    if (a.lse_out != nullptr && tid == 0) a.lse_out[r] = -INFINITY;
+    return;
+  }
+  const bool dense = T_ >= a.C;
+  const shared::Parts pp(dense, it, a.tile_prefix + it, pp_pairs);
+  const shared::Parts po(dense, b, a.tile_prefix + a.prefix_items + b, po_pairs);
+  if (a.prefix_items == 0 && po.n == 1) return;
+  if (dense) merge_row<T, kLanes, kGroups, true>(a, pp, po, r, b, T_);
+  else merge_row<T, kLanes, kGroups, false>(a, pp, po, r, b, T_);
 }
 
 // ---------------------------------------------------------------- narrow rows, few heads
@@ -310,6 +383,7 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
 #pragma unroll
     for (int e = 0; e < 4; ++e) oacc[j][e] = 0.f;
   float m_ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
+  float ldif[2] = {0.f, 0.f};  // what the rounding of the weights adds to their sum
   for (int st = 0; st < kStages - 1; ++st) {
     if (st < n_stages) issue_stage(st);
     cp_async_commit();
@@ -357,6 +431,7 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
         if (mx > m_ref[h2] + kLazy) {  // the quad agrees
           const float alpha = exp2f(m_ref[h2] - mx);
           lsum[h2] *= alpha;
+          ldif[h2] *= alpha;
 #pragma unroll
           for (int j = 0; j < kMaxND; ++j) {
             oacc[j][2 * h2] *= alpha;
@@ -366,10 +441,11 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
         }
 #pragma unroll
         for (int n8 = 0; n8 < 8; ++n8) {
-          // the denominator sums the weights before they are rounded to 16 bits
           const float p0 = exp2f(s[n8][2 * h2] - m_ref[h2]), p1 = exp2f(s[n8][2 * h2 + 1] - m_ref[h2]);
-          lsum[h2] += p0 + p1;
           const P2 two = Pack<T>::make(p0, p1);
+          const float2 back = Pack<T>::f2(two);
+          lsum[h2] += p0 + p1;
+          ldif[h2] += (back.x - p0) + (back.y - p1);
           s[n8][2 * h2] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&two));
         }
       }
@@ -393,12 +469,16 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
   cp_async_wait<0>();
 #pragma unroll
   for (int h2 = 0; h2 < 2; ++h2) {
-    float l = lsum[h2];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    // the lse from the weights before rounding (good to fp32), o over the sum of the rounded ones
+    float l = lsum[h2], dif = ldif[h2];
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      dif += __shfl_xor_sync(0xffffffffu, dif, o);
+    }
     if (rows[h2] >= R) continue;
     const bool some = live[h2] && l > 0.f;
-    const float inv = some ? 1.f / l : 0.f;
+    const float inv = some ? 1.f / (l + dif) : 0.f;
     const long part = (long)rows[h2] * g0.n_splits + split;
 #pragma unroll
     for (int j = 0; j < kMaxND; ++j)
