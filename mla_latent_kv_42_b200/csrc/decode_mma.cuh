@@ -166,15 +166,14 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
       stage_page[buf][tid] = pg;
     }
     __syncthreads();
-    const uint32_t base = sm_u32 + buf * kStageTokens * stride;
-    for (int c = tid; c < kStageTokens * chunks_per_row; c += 128) {
-      const int row = c / chunks_per_row, col = c - row * chunks_per_row;
-      const int tok = s0 + row;
-      const int pg = stage_page[buf][row >> 4];
-      const bool valid = tok < t1 && pg >= 0;
-      const T* src = valid ? pool + ((long)pg * page_size + tok % page_size) * D + col * 8 : pool;
-      cp_async16(base + row * stride + col * 16, src, valid ? 16u : 0u);
-    }
+    // two threads to a row: one slot computation per stage, then every other 16-byte chunk
+    const int row = tid >> 1, tok = s0 + row;
+    const int pg = stage_page[buf][row >> 4];
+    const bool valid = tok < t1 && pg >= 0;
+    const T* const src = valid ? pool + ((long)pg * page_size + tok % page_size) * D : pool;
+    const uint32_t dst = sm_u32 + (buf * kStageTokens + row) * stride;
+    for (int col = tid & 1; col < chunks_per_row; col += 2)
+      cp_async16(dst + col * 16, valid ? src + col * 8 : pool, valid ? 16u : 0u);
   };
 
   float oacc[kMaxND][4];

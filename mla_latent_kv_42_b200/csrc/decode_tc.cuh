@@ -150,6 +150,7 @@ constexpr int kItemUnits = 2;
 struct SharedTcParams : DecodeTcParams {
   const int* first;         // [B], -1 for a rejected sequence (which has no tiles)
   const int* shared_pages;  // pages of the prefix
+  const int* start;         // [C] item that each pair begins in
   int prefix_items, prefix_len;
   int own_q_rows;           // n_h rounded up to 8 where a sequence's rows fit one small box, else 0
   float* lse_pre;           // [items + C][128]
@@ -176,6 +177,11 @@ __device__ __forceinline__ ItemIter item_iter(const int* prefix, int B, int clus
   }
   it.b = lo;
   return it;
+}
+// The same with the item that the range begins in given.
+__device__ __forceinline__ ItemIter item_iter_at(const int* prefix, int B, int cluster, int nclusters, int b) {
+  const long T = prefix[B];
+  return ItemIter{T * cluster / nclusters, T * (cluster + 1) / nclusters, b};
 }
 // kUnits: places an item takes in the list before its tiles, for its share of the split (kItemUnits
 // below); 0 where the list holds tiles alone.
@@ -204,8 +210,10 @@ struct CursorOf {
   Item item;
   int t, ti, ii;
   bool valid;
-  __device__ __forceinline__ void start(const int* prefix, int B, int cluster, int nclusters) {
-    it = item_iter(prefix, B, cluster, nclusters);
+  __device__ __forceinline__ void start(const int* prefix, int B, int cluster, int nclusters,
+                                        const int* starts = nullptr) {
+    it = starts != nullptr ? item_iter_at(prefix, B, cluster, nclusters, starts[cluster])
+                           : item_iter(prefix, B, cluster, nclusters);
     valid = next_item<kUnits>(it, prefix, item);
     t = valid ? item.t0 : 0;
     ti = 0;
@@ -367,6 +375,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
     return ok;
   };
   const uint32_t set_u32 = data_u32 + kSetOff;
+  const int* starts = nullptr;
+  if constexpr (kShared) starts = p.start;
   // Item b's tokens, pages and first query row: sequence b itself, or (kShared) 128 packed rows
   // over the shared pages or a sequence's own tokens.
   auto item_len = [&](int b) {
@@ -411,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         }
         tma_prefetch_map(&maps.q9);
         Cursor c;
-        c.start(prefix, p.B, cluster, nclusters);
+        c.start(prefix, p.B, cluster, nclusters, starts);
         int L = 0;
         const int* btb = nullptr;
         while (c.valid) {
@@ -487,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
       // done with the own page's columns in those slots (a tail page with its zero-filled rows).
       if (lane == 0) {
         Cursor c;
-        c.start(prefix, p.B, cluster, nclusters);
+        c.start(prefix, p.B, cluster, nclusters, starts);
         int L = 0;
         const int* btb = nullptr;
         const int g = 1 - (int)rank;
@@ -552,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
           return false;
         };
         Cursor c;
-        c.start(prefix, p.B, cluster, nclusters);
+        c.start(prefix, p.B, cluster, nclusters, starts);
         if (warp == kMmaWarp) {
           // S(i) = Q C^T into S buffer i & 1
           const uint32_t q_lo = desc_sw128_lo(data_u32 + kQOff, 16);
@@ -771,7 +781,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
       };
       if constexpr (F8) {
         Cursor c;
-        c.start(prefix, p.B, cluster, nclusters);
+        c.start(prefix, p.B, cluster, nclusters, starts);
         int L = c.valid ? p.seq_lens[c.item.b] : 0;
         TileScales cur = c.valid ? tile_scales(c, L) : TileScales{};
         while (c.valid) {
@@ -835,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         return true;
       };
       Cursor c;
-      c.start(prefix, p.B, cluster, nclusters);
+      c.start(prefix, p.B, cluster, nclusters, starts);
       float m_ref = -INFINITY, lsum = 0.f;
       float ldif = 0.f;  // kShared: what the rounding of the weights adds to their sum
       int L = 0;

@@ -453,11 +453,9 @@ rows::SlotMap slot_map(const mla_dims* d, const int32_t* bt, int32_t num_seqs, i
   return rows::SlotMap{bt, (int)num_seqs, (int)max_pages, (int)num_pages, (int)d->page_size};
 }
 
-// CTAs for T tokens, `per_warp` of them a warp at a time: one wave of eight CTAs per SM at most,
-// then the warps loop.
-unsigned rows_grid(int T, int per_warp) {
-  const long need = ((long)T + (long)rows::kWarps * per_warp - 1) / ((long)rows::kWarps * per_warp);
-  return (unsigned)std::min<long>(need, 8L * device_sm_count());
+// CTAs for T tokens, a warp each, and `per_sm` CTAs to an SM at most.
+unsigned rows_grid(int T, int per_sm) {
+  return (unsigned)std::min<long>(((long)T + rows::kWarps - 1) / rows::kWarps, (long)per_sm * device_sm_count());
 }
 
 template <typename T, bool kFp8>
@@ -480,8 +478,11 @@ int norm_append_impl(const mla_dims* d, const void* x, int64_t x_stride, const v
   a.turns.table = d->rope_inv_freq;
   double r = std::pow(d->rope_base, -2.0 / (double)d->d_rope);
   for (int j = 0; j < rows::kPowers; ++j, r *= r) a.turns.pw[j] = r;
-  if (launch_pdl(k_norm_append<T, kFp8>, dim3(rows_grid(T_, 1)), dim3(32 * rows::kWarps), 0, st, a) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  const dim3 grid(rows_grid(T_, rows::kAppendPerSm)), block(32 * rows::kWarps);
+  // one pair of the rotated part to a lane where that is enough: the arrays for nine cost registers
+  const cudaError_t e = d->d_rope <= 64 ? launch_pdl(k_norm_append<T, kFp8, 1>, grid, block, 0, st, a)
+                                        : launch_pdl(k_norm_append<T, kFp8, rows::kMaxR>, grid, block, 0, st, a);
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
   return finish_launches(kFp8 ? MLA_CALL_NORM_APPEND_KV_FP8 : MLA_CALL_NORM_APPEND_KV, 1);
 }
 
@@ -524,7 +525,7 @@ int read_kv_call(const mla_dims* d, const void* pool, int32_t num_pages, const i
   if (!aligned16(pool) || !aligned16(out)) return MLA_ERR_ALIGNMENT;
   const rows::ReadArgs a{pool, seq_idx, pos, slot_map(d, bt, num_seqs, max_pages, num_pages), (int)d->d_c,
                          (int)(d->d_c + d->d_rope), (int)T, out, (long)out_stride};
-  const dim3 grid(rows_grid(T, rows::kReadTokens)), block(32 * rows::kWarps);
+  const dim3 grid(rows_grid(T, rows::kReadPerSm)), block(32 * rows::kWarps);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = d->dtype == MLA_BF16 ? launch_pdl(k_read_rows<__nv_bfloat16, kFp8>, grid, block, 0, st, a)
                                              : launch_pdl(k_read_rows<__half, kFp8>, grid, block, 0, st, a);
@@ -547,7 +548,7 @@ bool shared_packs(const mla_dims* d, int B) {
 
 struct SharedTcLayout {
   int Mt;  // packed row tiles
-  size_t first, len, tile_prefix, pairs, o_pre, lse_pre, o_part, lse_part, bytes;
+  size_t first, len, tile_prefix, pairs, start, o_pre, lse_pre, o_part, lse_part, bytes;
 };
 SharedTcLayout shared_tc_layout(const mla_dims* d, int B, bool packed) {
   SharedTcLayout L;
@@ -564,6 +565,7 @@ SharedTcLayout shared_tc_layout(const mla_dims* d, int B, bool packed) {
   L.len = take((size_t)B * 4);
   L.tile_prefix = take(((size_t)L.Mt + B + 1) * 4);
   L.pairs = take(((size_t)L.Mt + B) * 4);
+  L.start = take(C * 4);
   L.o_pre = take(pre_rows * tc::dec::kDc * 4);
   L.lse_pre = take(pre_rows * 4);
   L.o_part = take(own_rows * tc::dec::kDc * 4);
@@ -577,7 +579,8 @@ SharedTcLayout shared_tc_layout(const mla_dims* d, int B, bool packed) {
 struct SharedMmaPlan {
   int row_tiles, pre_splits, pre_split_len, own_splits, own_split_len;
 };
-constexpr int kSharedMinStages = 4;  // stages of a prefix split at least
+
+constexpr int kSharedMinStages = 2;
 int shared_splits(long items, long stages, long min_stages, int* split_len) {
   long s = std::max(1L, 3L * device_sm_count() / items);
   s = std::min(s, std::max(1L, (stages + min_stages - 1) / min_stages));
@@ -626,6 +629,7 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   plan.len = reinterpret_cast<int*>(ws + L.len);
   plan.tile_prefix = reinterpret_cast<int*>(ws + L.tile_prefix);
   plan.pairs = reinterpret_cast<int*>(ws + L.pairs);
+  plan.start = reinterpret_cast<int*>(ws + L.start);
   plan.C = C;
   float* o_pre = reinterpret_cast<float*>(ws + L.o_pre);
   float* o_part = reinterpret_cast<float*>(ws + L.o_part);
@@ -667,6 +671,7 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   p.f8_pool = nullptr;
   p.first = plan.first;
   p.shared_pages = plan.shared_pages;
+  p.start = plan.start;
   p.prefix_items = L.Mt;
   p.prefix_len = plan.n_shared * plan.page_size;
   p.own_q_rows = own_q_rows;
@@ -685,25 +690,37 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   return MLA_OK;
 }
 
-template <typename T>
+// Shared memory of the narrow-row kernel: its stages have rows of KDC k steps, as long as the
+// rows of the own items' or longer.
+template <int KDC>
+constexpr size_t shared_mma_smem() {
+  return dmma::smem_bytes(16 * KDC);
+}
+
+template <typename T, int KDC>
 bool shared_mma_set_smem() {
   static std::atomic<bool> done[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
   if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(k_shared_mma<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)dmma::smem_bytes(16 * dmma::kMaxKD)) != cudaSuccess)
+    if (cudaFuncSetAttribute(k_shared_mma<T, KDC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)shared_mma_smem<KDC>()) != cudaSuccess)
       return false;
     done[dev].store(true, std::memory_order_release);
   }
   return true;
 }
 
+template <typename T, int KDC>
+bool launch_shared_mma(const shared::MmaArgs& a, unsigned blocks, cudaStream_t st) {
+  return shared_mma_set_smem<T, KDC>() &&
+         launch_pdl(k_shared_mma<T, KDC>, dim3(blocks), dim3(128), shared_mma_smem<KDC>(), st, a) == cudaSuccess;
+}
+
 template <typename T>
 int shared_mma_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_pages, shared::PlanArgs& plan,
                     void* o_lat, float* lse_out, char* ws, cudaStream_t st, int32_t& launches) {
   const int B = plan.B, D = d->d_c + d->d_rope, shared_len = plan.n_shared * plan.page_size;
-  if (!shared_mma_set_smem<T>()) return MLA_ERR_CUDA;
   const SharedMmaPlan s = shared_mma_plan(d, B, shared_len, plan.max_seq_len);
   const int parts = s.pre_splits + s.own_splits;
   const long R = (long)B * d->n_heads;
@@ -725,8 +742,16 @@ int shared_mma_impl(const mla_dims* d, const void* q, const void* pool, int32_t 
   a.pre_split_len = s.pre_split_len;
   a.own_splits = s.own_splits;
   const long blocks = (long)s.row_tiles * s.pre_splits + (long)B * s.own_splits;
-  if (launch_pdl(k_shared_mma<T>, dim3((unsigned)blocks), dim3(128), dmma::smem_bytes(D), st, a) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  bool ok = false;
+  switch ((D + 31) / 32) {  // D <= 192
+    case 1: ok = launch_shared_mma<T, 2>(a, (unsigned)blocks, st); break;
+    case 2: ok = launch_shared_mma<T, 4>(a, (unsigned)blocks, st); break;
+    case 3: ok = launch_shared_mma<T, 6>(a, (unsigned)blocks, st); break;
+    case 4: ok = launch_shared_mma<T, 8>(a, (unsigned)blocks, st); break;
+    case 5: ok = launch_shared_mma<T, 10>(a, (unsigned)blocks, st); break;
+    default: ok = launch_shared_mma<T, 12>(a, (unsigned)blocks, st); break;
+  }
+  if (!ok) return MLA_ERR_CUDA;
   launches += 2;
   if (parts > 1) {
     if (launch_pdl(k_lse_merge_warp<T>, dim3((unsigned)((R + 7) / 8)), dim3(256), 0, st,

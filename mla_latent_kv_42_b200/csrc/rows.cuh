@@ -16,10 +16,15 @@
 namespace mla {
 namespace rows {
 constexpr int kGroups = 3;    // 8-element groups per lane: D <= 768
-constexpr int kMaxPairs = 284;  // d_rope / 2
-constexpr int kPowers = 9;      // kMaxPairs < 2^9
+constexpr int kLatGroups = 2; // 8-element groups of the latent part per lane: d_c <= 512
+constexpr int kMaxR = 9;      // pairs of the rotated part per lane: d_rope / 2 <= 284 <= 32 kMaxR
+constexpr int kPowers = 9;    // 32 kMaxR < 2^9
 constexpr int kWarps = 8;     // per CTA
-constexpr int kReadTokens = 4;  // tokens a warp of k_read_rows has in flight
+// CTAs per SM at most; warps then loop over tokens. A writer keeps its registers (gains, frequencies)
+// and requests a token ahead: four CTAs fit, more only repeat its start (8192 tokens: 7.3 us with
+// three or four, 8.2 with eight). A reader has nothing to keep (131072 tokens: 44.5 us; with two
+// or four tokens to a warp at a time 43.8 to 46, but 1021 tokens 2.6 and 3.2 us against 2.2).
+constexpr int kAppendPerSm = 4, kReadPerSm = 32;
 
 // Slot (row of the pool) of position p of sequence s, or -1 if it is outside the table or the pool.
 struct SlotMap {
@@ -84,28 +89,40 @@ struct AppendArgs {
 }  // namespace rows
 
 // A warp per token, the next token's row, position and sequence requested before this one's
-// arithmetic. The frequencies are formed once per CTA in shared memory (they are doubles), and the
-// warp's lanes share a token's cosines and sines, one pair each, through it.
-template <typename T, bool kFp8>
+// arithmetic. A lane holds kC groups of 8 latent values and kR pairs of the rotated part: one pair
+// to a lane at d_rope <= 64, so that a token's cosines and sines are formed by 32 lanes at once.
+// What a lane needs of the gains and the frequencies (doubles) is the same for every token and
+// stays in its registers.
+template <typename T, bool kFp8, int kR>
 __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::AppendArgs a) {
   using namespace rows;
   using P2 = typename Pack<T>::T2;
-  __shared__ double s_turns[kMaxPairs];
-  __shared__ float2 s_cs[kWarps][kMaxPairs];
+  constexpr int kC = kLatGroups;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = a.D / 8, Gc = a.d_c / 8;  // groups of the row, of its latent part
-  const int pairs = (a.D - a.d_c) / 2;
-  if (a.turns.table == nullptr)  // from the arguments alone: ahead of the wait
-    for (int k = threadIdx.x; k < pairs; k += 32 * kWarps) s_turns[k] = a.turns(k);
+  const int Gc = a.d_c / 8, pairs = (a.D - a.d_c) / 2;
+  double turns[kR];
+#pragma unroll
+  for (int j = 0; j < kR; ++j)  // from the arguments alone: ahead of the wait
+    turns[j] = a.turns.table == nullptr ? a.turns(lane + 32 * j) : 0.0;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
-  if (a.turns.table != nullptr)
-    for (int k = threadIdx.x; k < pairs; k += 32 * kWarps) s_turns[k] = a.turns(k);
-  __syncthreads();
-  float2* const cs = s_cs[warp];
+  uint4 gc[kC];
+  uint32_t gr[kR];
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+    gc[i] = a.g_c != nullptr && lane + 32 * i < Gc ? ldg16(static_cast<const T*>(a.g_c) + 8 * (lane + 32 * i))
+                                                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < kR; ++j) {
+    const int k = lane + 32 * j;
+    gr[j] = a.g_r != nullptr && k < pairs ? __ldg(static_cast<const uint32_t*>(a.g_r) + k) : 0u;
+    if (a.turns.table != nullptr && k < pairs) turns[j] = a.turns(k);
+  }
+  auto two = [](uint32_t w) { return Pack<T>::f2(*reinterpret_cast<const P2*>(&w)); };
   const int n_warps = gridDim.x * kWarps;
   int t = blockIdx.x * kWarps + warp;
-  uint4 raw[kGroups];
+  uint4 raw_c[kC];
+  uint32_t raw_r[kR];
   int p = 0, seq = 0;
   auto request = [&](int tt) {
     if (tt >= a.T) return;
@@ -113,86 +130,88 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
     p = a.pos[tt];
     seq = a.seq_idx[tt];
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int g = lane + 32 * i;
-      raw[i] = g < G ? *reinterpret_cast<const uint4*>(src + 8 * g) : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < kC; ++i)
+      raw_c[i] = lane + 32 * i < Gc ? *reinterpret_cast<const uint4*>(src + 8 * (lane + 32 * i)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < kR; ++j)
+      raw_r[j] = lane + 32 * j < pairs ? *reinterpret_cast<const uint32_t*>(src + a.d_c + 2 * (lane + 32 * j)) : 0u;
   };
   request(t);
   for (; t < a.T; t += n_warps) {
     const int pos = p;
-    const long slot = a.slot(seq, pos);
-    float v[kGroups][8];
+    const long slot = a.slot(seq, pos);  // used at the end: the table's read overlaps the arithmetic
+    float v[kC][8];
+    float2 r[kR];
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) unpack8<T>(raw[i], v[i]);
+    for (int i = 0; i < kC; ++i) unpack8<T>(raw_c[i], v[i]);
+#pragma unroll
+    for (int j = 0; j < kR; ++j) r[j] = two(raw_r[j]);
     request(t + n_warps);
+    if (a.g_c != nullptr) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < kC; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+      const float rs = rsqrtf(warp_sum(ss) / (float)a.d_c + a.eps);
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        float gf[8];
+        unpack8<T>(gc[i], gf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * rs * gf[e];
+      }
+    }
+    if (a.g_r != nullptr) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < kR; ++j) ss = fmaf(r[j].x, r[j].x, fmaf(r[j].y, r[j].y, ss));
+      const float rs = rsqrtf(warp_sum(ss) / (float)(a.D - a.d_c) + a.eps);
+#pragma unroll
+      for (int j = 0; j < kR; ++j) {
+        const float2 g = two(gr[j]);
+        r[j] = make_float2(r[j].x * rs * g.x, r[j].y * rs * g.y);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kR; ++j) {
+      float c, s;
+      turn_cos_sin(pos, turns[j], c, s);
+      r[j] = make_float2(r[j].x * c - r[j].y * s, r[j].x * s + r[j].y * c);
+    }
+    float mc = 0.f, mr = 0.f;
+    if constexpr (kFp8) {  // non-negative floats order as their bit patterns
+#pragma unroll
+      for (int i = 0; i < kC; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mc = fmaxf(mc, fabsf(v[i][e]));
+#pragma unroll
+      for (int j = 0; j < kR; ++j) mr = fmaxf(mr, fmaxf(fabsf(r[j].x), fabsf(r[j].y)));
+      mc = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mc)));
+      mr = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mr)));
+    }
     if (slot < 0) {
       if (lane == 0) record_error(MLA_ERR_BAD_PAGE);
       continue;
     }
-    for (int k = lane; k < pairs; k += 32) turn_cos_sin(pos, s_turns[k], cs[k].x, cs[k].y);
-    float ss_c = 0.f, ss_r = 0.f;
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-      if (lane + 32 * i < Gc) ss_c += ss;
-      else ss_r += ss;
-    }
-    if (a.g_c != nullptr) ss_c = rsqrtf(warp_sum(ss_c) / (float)a.d_c + a.eps);
-    if (a.g_r != nullptr) ss_r = rsqrtf(warp_sum(ss_r) / (float)(a.D - a.d_c) + a.eps);
-    __syncwarp();  // cs is written
-    float mc = 0.f, mr = 0.f;
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int g = lane + 32 * i;
-      const bool lat = g < Gc;
-      const void* gain = lat ? a.g_c : a.g_r;
-      if (gain != nullptr && g < G) {
-        float gf[8];
-        unpack8<T>(ldg16(static_cast<const T*>(gain) + 8 * (lat ? g : g - Gc)), gf);
-        const float rs = lat ? ss_c : ss_r;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * rs * gf[e];
-      }
-      if (!lat && g < G) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 c = cs[4 * (g - Gc) + e];
-          const float x0 = v[i][2 * e], x1 = v[i][2 * e + 1];
-          v[i][2 * e] = x0 * c.x - x1 * c.y;
-          v[i][2 * e + 1] = x0 * c.y + x1 * c.x;
-        }
-      }
-      if constexpr (kFp8) {
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[i][e]));
-        if (lat) mc = fmaxf(mc, m);
-        else mr = fmaxf(mr, m);
-      }
-    }
-    __syncwarp();  // cs has been read
     if constexpr (!kFp8) {
       T* dst = static_cast<T*>(a.pool) + slot * a.D;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int g = lane + 32 * i;
-        if (g < G) {
+      for (int i = 0; i < kC; ++i)
+        if (lane + 32 * i < Gc) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const P2 two = Pack<T>::make(v[i][2 * e], v[i][2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&two);
+            const P2 pk = Pack<T>::make(v[i][2 * e], v[i][2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&pk);
           }
-          *reinterpret_cast<uint4*>(dst + 8 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(dst + 8 * (lane + 32 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-      }
+#pragma unroll
+      for (int j = 0; j < kR; ++j)
+        if (lane + 32 * j < pairs)
+          *reinterpret_cast<P2*>(dst + a.d_c + 2 * (lane + 32 * j)) = Pack<T>::make(r[j].x, r[j].y);
     } else {
-      // non-negative floats order as their bit patterns
-      mc = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mc)));
-      mr = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mr)));
       const float sc = mc > 0.f ? mc / fp8::kE4m3Max : 1.f;
       const float sr = mr > 0.f ? mr / fp8::kE4m3Max : 1.f;
       const float ic = 1.f / sc, ir = 1.f / sr;
@@ -202,25 +221,24 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
       const long page = slot / ps;
       const int row = (int)(slot - page * ps);
       uint8_t* const pg = static_cast<uint8_t*>(a.pool) + page * fp8::page_bytes(ps, a.D);
+      uint8_t* const dst = pg + (long)row * a.D;
       auto store = [&](auto divide) {
+        auto e4m3x2 = [&](float x, float y, float s, float inv) {
+          return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(divide(x, s, inv), divide(y, s, inv)), __NV_SATFINITE,
+                                                    __NV_E4M3);
+        };
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-          const int g = lane + 32 * i;
-          if (g < G) {
-            const float s = g < Gc ? sc : sr, inv = g < Gc ? ic : ir;
-            uint32_t q[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float* x = v[i] + 4 * h;
-              const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-                  make_float2(divide(x[0], s, inv), divide(x[1], s, inv)), __NV_SATFINITE, __NV_E4M3);
-              const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-                  make_float2(divide(x[2], s, inv), divide(x[3], s, inv)), __NV_SATFINITE, __NV_E4M3);
-              q[h] = (uint32_t)lo | ((uint32_t)hi << 16);
-            }
-            *reinterpret_cast<uint2*>(pg + (long)row * a.D + 8 * g) = make_uint2(q[0], q[1]);
+        for (int i = 0; i < kC; ++i)
+          if (lane + 32 * i < Gc) {
+            const float* x = v[i];
+            *reinterpret_cast<uint2*>(dst + 8 * (lane + 32 * i)) =
+                make_uint2(e4m3x2(x[0], x[1], sc, ic) | (e4m3x2(x[2], x[3], sc, ic) << 16),
+                           e4m3x2(x[4], x[5], sc, ic) | (e4m3x2(x[6], x[7], sc, ic) << 16));
           }
-        }
+#pragma unroll
+        for (int j = 0; j < kR; ++j)
+          if (lane + 32 * j < pairs)
+            *reinterpret_cast<uint16_t*>(dst + a.d_c + 2 * (lane + 32 * j)) = (uint16_t)e4m3x2(r[j].x, r[j].y, sr, ir);
       };
       if (plain) store([](float x, float s, float) { return x / s; });
       else store([](float x, float s, float inv) { return quotient(x, s, inv); });
@@ -241,9 +259,9 @@ struct ReadArgs {
 };
 }  // namespace rows
 
-// A warp takes kReadTokens consecutive tokens at a time: lanes 0 .. kReadTokens - 1 look up their
-// slots (three dependent reads, once for the group), then every lane has the loads of all of them
-// in flight. A token without a valid slot becomes a zero row and records MLA_ERR_BAD_PAGE.
+// A warp per token. Bound by the writes: 151 MB of rows out of 76 MB of e4m3 pages take 44.5 us, and
+// setting 151 MB to zero takes 41.5 (3.6 TB/s; reads run beside it). A token without a valid slot
+// becomes a zero row and records MLA_ERR_BAD_PAGE.
 template <typename T, bool kFp8>
 __global__ void __launch_bounds__(32 * rows::kWarps) k_read_rows(const rows::ReadArgs a) {
   using namespace rows;
@@ -254,63 +272,51 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_read_rows(const rows::Rea
   const int ps = a.slot.page_size;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
-  const long n_warps = (long)gridDim.x * kWarps;
-  for (long t0 = ((long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kReadTokens; t0 < a.T;
-       t0 += n_warps * kReadTokens) {
-    long mine = -1;
-    if (lane < kReadTokens && t0 + lane < a.T) {
-      mine = a.slot(a.seq_idx[t0 + lane], a.pos[t0 + lane]);
-      if (mine < 0) record_error(MLA_ERR_BAD_PAGE);
+  const int n_warps = gridDim.x * kWarps;
+  for (int t = blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += n_warps) {
+    const long slot = a.slot(a.seq_idx[t], a.pos[t]);
+    if (slot < 0 && lane == 0) record_error(MLA_ERR_BAD_PAGE);
+    Raw raw[kGroups];
+    float2 sc = make_float2(0.f, 0.f);
+    const uint8_t* src;
+    if constexpr (kFp8) {
+      const long page = slot / ps;
+      const int row = (int)(slot - page * ps);
+      const uint8_t* pg = static_cast<const uint8_t*>(a.pool) + page * fp8::page_bytes(ps, a.D);
+      src = pg + (long)row * a.D;
+      if (slot >= 0) sc = *reinterpret_cast<const float2*>(pg + (long)ps * a.D + 8 * row);
+    } else {
+      src = static_cast<const uint8_t*>(a.pool) + slot * a.D * (long)sizeof(T);
     }
-    Raw raw[kReadTokens][kGroups];
-    float2 sc[kReadTokens];
 #pragma unroll
-    for (int u = 0; u < kReadTokens; ++u) {
-      const long slot = __shfl_sync(0xffffffffu, mine, u);
-      const uint8_t* src;
+    for (int i = 0; i < kGroups; ++i) {
+      const int g = lane + 32 * i;
+      raw[i] = slot >= 0 && g < G ? *reinterpret_cast<const Raw*>(src + sizeof(Raw) * g) : Raw{};
+    }
+    T* dst = static_cast<T*>(a.out) + (long)t * a.out_stride;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int g = lane + 32 * i;
+      if (g >= G) continue;
+      uint4 o;
       if constexpr (kFp8) {
-        const long page = slot / ps;
-        const int row = (int)(slot - page * ps);
-        const uint8_t* pg = static_cast<const uint8_t*>(a.pool) + page * fp8::page_bytes(ps, a.D);
-        src = pg + (long)row * a.D;
-        sc[u] = slot >= 0 ? *reinterpret_cast<const float2*>(pg + (long)ps * a.D + 8 * row) : make_float2(0.f, 0.f);
-      } else {
-        src = static_cast<const uint8_t*>(a.pool) + slot * a.D * (long)sizeof(T);
-      }
+        // value = scale * e4m3 in fp32 (the e4m3 value is exact in fp16), rounded once
+        const float s = g < Gc ? sc.x : sc.y;
+        const uint32_t in[2] = {raw[i].x, raw[i].y};
+        uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int g = lane + 32 * i;
-        raw[u][i] = slot >= 0 && g < G ? *reinterpret_cast<const Raw*>(src + sizeof(Raw) * g) : Raw{};
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kReadTokens; ++u) {
-      if (t0 + u >= a.T) break;
-      T* dst = static_cast<T*>(a.out) + (t0 + u) * a.out_stride;
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int g = lane + 32 * i;
-        if (g >= G) continue;
-        uint4 o;
-        if constexpr (kFp8) {
-          // value = scale * e4m3 in fp32 (the e4m3 value is exact in fp16), rounded once
-          const float s = g < Gc ? sc[u].x : sc[u].y;
-          const uint32_t in[2] = {raw[u][i].x, raw[u][i].y};
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2_raw hr =
-                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-            const P2 two = Pack<T>::make(f.x * s, f.y * s);
-            w[e] = *reinterpret_cast<const uint32_t*>(&two);
-          }
-          o = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-          o = raw[u][i];
+        for (int e = 0; e < 4; ++e) {
+          const __half2_raw hr =
+              __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+          const P2 two = Pack<T>::make(f.x * s, f.y * s);
+          w[e] = *reinterpret_cast<const uint32_t*>(&two);
         }
-        *reinterpret_cast<uint4*>(dst + 8 * g) = o;
+        o = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        o = raw[i];
       }
+      *reinterpret_cast<uint4*>(dst + 8 * g) = o;
     }
   }
 }

@@ -31,6 +31,7 @@ struct PlanArgs {
   int* tile_prefix;  // [prefix_items + B + 1] places before each item in the list of the items'
                      // tiles, kItemUnits places and then its tiles to an item that has any; or null
   int* pairs;        // [prefix_items + B] first and last pair of an item's tiles, c0 | c1 << 16, -1: none
+  int* start;        // [C] item that each pair begins in
   int C;             // pairs
 };
 }  // namespace shared
@@ -43,6 +44,7 @@ struct PlanArgs {
 __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) {
   __shared__ int s_count[shared::kScanSeqs];
   __shared__ int warp_total[32];
+  __shared__ int s_run[1024];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
     return pair_of(begin + tc::kItemUnits) | (pair_of(begin + n - 1) << 16);
   };
   for (int i = tid; i < a.prefix_items; i += 1024) a.pairs[i] = pairs_of(i * nt, nt);
+  s_run[tid] = a.prefix_items * nt + incl - sum + (warp > 0 ? warp_total[warp - 1] : 0);
   int run = a.prefix_items * nt + incl - sum + (warp > 0 ? warp_total[warp - 1] : 0);
   for (int b = b0; b < b1; ++b) {
     const int n = count[b];  // read before the same place may be overwritten
@@ -139,6 +142,22 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
     run += n;
   }
   if (tid == 1023) mine[a.B] = (int)T;
+  __syncthreads();
+  if (tid < a.C) {  // the item that pair tid begins in, or one before it whose places end there
+    const int g = (int)(T * tid / a.C);
+    if (g < a.prefix_items * nt) {
+      a.start[tid] = g / nt;
+    } else {
+      int lo = 0, hi = 1023;  // the last thread whose sequences begin at or before g
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_run[mid] <= g) lo = mid; else hi = mid - 1;
+      }
+      int b = min(lo * per, a.B - 1);
+      while (b + 1 < a.B && mine[b + 1] <= g) ++b;
+      a.start[tid] = a.prefix_items + b;
+    }
+  }
 }
 
 namespace shared {
@@ -328,8 +347,10 @@ struct MmaArgs {
 // Tokens [t0, t1) of the prefix for query rows [row0, row0 + 64): each warp holds 16 rows (A
 // fragments of Q, fp32 O) and runs over all 64 tokens of a stage, so a stage that one sequence's
 // heads would use once serves 64 rows. The arithmetic is attn_mma_item's: P stays in registers as
-// the A fragment of the value product.
-template <typename T>
+// the A fragment of the value product. KDC: k steps of the score product, the row's rounded up to 32
+// columns. With the shared-memory row stride a constant every ldmatrix address is a base and an
+// immediate, and a step past the row's end multiplies by zeros of Q (columns read again there).
+template <typename T, int KDC>
 __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, uint8_t* sm) {
   using namespace dmma;
   using P2 = typename Pack<T>::T2;
@@ -338,7 +359,7 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
   const int R = g0.B * g0.n_h;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, tq = lane & 3;
-  const int stride = row_stride(D);
+  constexpr int stride = row_stride(16 * KDC);
   const uint32_t sm_u32 = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
   const T* __restrict__ q = static_cast<const T*>(g0.q);
   const T* __restrict__ pool = static_cast<const T*>(g0.pool);
@@ -351,30 +372,31 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
   for (int e = 0; e < 2; ++e) live[e] = rows[e] < R && g0.first[rows[e] / g0.n_h] > 0;
   const bool warp_live = __any_sync(0xffffffffu, live[0] || live[1]);
 
-  uint32_t qa[kMaxKD][4];
+  uint32_t qa[KDC][4];
 #pragma unroll
-  for (int ks = 0; ks < kMaxKD; ++ks)
+  for (int ks = 0; ks < KDC; ++ks)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int row = rows[e & 1], col = 16 * ks + 2 * tq + ((e & 2) ? 8 : 0);
       qa[ks][e] = ks < KD && row < R ? __ldg(reinterpret_cast<const unsigned*>(q + (long)row * D + col)) : 0u;
     }
 
-  // pages are looked up by each 16-token group's threads (page_size % 16 == 0) and were checked by
-  // the plan; an id outside the pool reads as zeros
-  const int chunks = D / 8;
+  // two threads to a row, each every other 16-byte chunk of it. The pages were checked by the plan;
+  // an id outside the pool reads as zeros. A stage's page id is requested a stage ahead.
+  const int chunks = D / 8, my_row = tid >> 1;
+  auto page_of = [&](int st) {
+    const int tok = t0 + st * kStageTokens + my_row;
+    return tok < t1 ? __ldg(a.shared_pages + tok / g0.page_size) : -1;
+  };
+  int pg_next = page_of(0);
   auto issue_stage = [&](int st) {
-    const uint32_t base = sm_u32 + (st % kStages) * kStageTokens * stride;
-    const int s0 = t0 + st * kStageTokens;
-    for (int c = tid; c < kStageTokens * chunks; c += 128) {
-      const int row = c / chunks, col = c - row * chunks;
-      const int tok = s0 + row;
-      int pg = -1;
-      if (tok < t1) pg = __ldg(a.shared_pages + tok / g0.page_size);
-      const bool valid = pg >= 0 && pg < g0.num_pages;
-      const T* src = valid ? pool + ((long)pg * g0.page_size + tok % g0.page_size) * D + col * 8 : pool;
-      cp_async16(base + row * stride + col * 16, src, valid ? 16u : 0u);
-    }
+    const int tok = t0 + st * kStageTokens + my_row, pg = pg_next;
+    pg_next = page_of(st + 1);
+    const bool valid = pg >= 0 && pg < g0.num_pages;
+    const T* const src = valid ? pool + ((long)pg * g0.page_size + tok % g0.page_size) * D : pool;
+    const uint32_t dst = sm_u32 + ((st % kStages) * kStageTokens + my_row) * stride;
+    for (int col = tid & 1; col < chunks; col += 2)
+      cp_async16(dst + col * 16, valid ? src + col * 8 : pool, valid ? 16u : 0u);
   };
 
   float oacc[kMaxND][4];
@@ -383,18 +405,23 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
 #pragma unroll
     for (int e = 0; e < 4; ++e) oacc[j][e] = 0.f;
   float m_ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
-  float ldif[2] = {0.f, 0.f};  // what the rounding of the weights adds to their sum
+  float rsum[2] = {0.f, 0.f};  // lsum of the rounded weights
   for (int st = 0; st < kStages - 1; ++st) {
     if (st < n_stages) issue_stage(st);
     cp_async_commit();
   }
   const int mi = lane >> 3, ri = lane & 7;
+  // ldmatrix rows of this lane: keys of the score product, values of the other (transposed)
+  const uint32_t k_lane = sm_u32 + (ri + 8 * (mi >> 1)) * stride + 16 * (mi & 1);
+  const uint32_t v_lane = sm_u32 + (ri + 8 * (mi & 1)) * stride + 16 * (mi >> 1);
+  const int last_k = 32 * (KD - 1);  // byte offset of the row's last k step
   for (int st = 0; st < n_stages; ++st) {
     if (st + kStages - 1 < n_stages) issue_stage(st + kStages - 1);
     cp_async_commit();
     cp_async_wait<kStages - 1>();
     __syncthreads();
-    const uint32_t tile_u32 = sm_u32 + (st % kStages) * kStageTokens * stride;
+    const uint32_t buf = (st % kStages) * kStageTokens * stride;
+    const uint32_t kb = k_lane + buf, vb = v_lane + buf;
     const int s0 = t0 + st * kStageTokens;
     if (warp_live) {
       float s[8][4];
@@ -403,35 +430,34 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n8][e] = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < kMaxKD; ++ks) {
-        if (ks < KD) {
+      for (int ks = 0; ks < KDC; ++ks) {
+        const uint32_t at = kb + (ks < KDC - 1 ? 32 * ks : last_k);  // D > 32 (KDC / 2 - 1)
 #pragma unroll
-          for (int n16 = 0; n16 < 4; ++n16) {
-            uint32_t bfr[4];
-            ldsm_x4(tile_u32 + (16 * n16 + ri + 8 * (mi >> 1)) * stride + (16 * ks + 8 * (mi & 1)) * 2, bfr);
-            mma16816<T>(s[2 * n16], qa[ks], bfr[0], bfr[1]);
-            mma16816<T>(s[2 * n16 + 1], qa[ks], bfr[2], bfr[3]);
-          }
+        for (int n16 = 0; n16 < 4; ++n16) {
+          uint32_t bfr[4];
+          ldsm_x4(at + 16 * n16 * stride, bfr);
+          mma16816<T>(s[2 * n16], qa[ks], bfr[0], bfr[1]);
+          mma16816<T>(s[2 * n16 + 1], qa[ks], bfr[2], bfr[3]);
         }
       }
-      const int left = t1 - s0;  // tokens of the stage that count
+      if (t1 - s0 < kStageTokens) {  // the prefix's last stage
+#pragma unroll
+        for (int n8 = 0; n8 < 8; ++n8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (8 * n8 + 2 * tq + (e & 1) >= t1 - s0) s[n8][e] = -INFINITY;
+      }
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int n8 = 0; n8 < 8; ++n8)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& v = s[n8][2 * h2 + e];
-            v = 8 * n8 + 2 * tq + e < left ? v * g0.scale_log2 : -INFINITY;
-            mx = fmaxf(mx, v);
-          }
+        for (int n8 = 0; n8 < 8; ++n8) mx = fmaxf(mx, fmaxf(s[n8][2 * h2], s[n8][2 * h2 + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * g0.scale_log2;
         if (mx > m_ref[h2] + kLazy) {  // the quad agrees
           const float alpha = exp2f(m_ref[h2] - mx);
           lsum[h2] *= alpha;
-          ldif[h2] *= alpha;
+          rsum[h2] *= alpha;
 #pragma unroll
           for (int j = 0; j < kMaxND; ++j) {
             oacc[j][2 * h2] *= alpha;
@@ -441,11 +467,12 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
         }
 #pragma unroll
         for (int n8 = 0; n8 < 8; ++n8) {
-          const float p0 = exp2f(s[n8][2 * h2] - m_ref[h2]), p1 = exp2f(s[n8][2 * h2 + 1] - m_ref[h2]);
+          const float p0 = tc::ex2_approx(fmaf(s[n8][2 * h2], g0.scale_log2, -m_ref[h2]));
+          const float p1 = tc::ex2_approx(fmaf(s[n8][2 * h2 + 1], g0.scale_log2, -m_ref[h2]));
           const P2 two = Pack<T>::make(p0, p1);
           const float2 back = Pack<T>::f2(two);
           lsum[h2] += p0 + p1;
-          ldif[h2] += (back.x - p0) + (back.y - p1);
+          rsum[h2] += back.x + back.y;
           s[n8][2 * h2] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&two));
         }
       }
@@ -457,7 +484,7 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
         for (int jp = 0; jp < kMaxND / 2; ++jp) {
           if (2 * jp < ND) {
             uint32_t bfr[4];
-            ldsm_x4_t(tile_u32 + (16 * k16 + ri + 8 * (mi & 1)) * stride + (16 * jp + 8 * (mi >> 1)) * 2, bfr);
+            ldsm_x4_t(vb + 16 * k16 * stride + 32 * jp, bfr);
             mma16816<T>(oacc[2 * jp], pa, bfr[0], bfr[1]);
             mma16816<T>(oacc[2 * jp + 1], pa, bfr[2], bfr[3]);
           }
@@ -470,15 +497,15 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
 #pragma unroll
   for (int h2 = 0; h2 < 2; ++h2) {
     // the lse from the weights before rounding (good to fp32), o over the sum of the rounded ones
-    float l = lsum[h2], dif = ldif[h2];
+    float l = lsum[h2], rounded = rsum[h2];
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       l += __shfl_xor_sync(0xffffffffu, l, o);
-      dif += __shfl_xor_sync(0xffffffffu, dif, o);
+      rounded += __shfl_xor_sync(0xffffffffu, rounded, o);
     }
     if (rows[h2] >= R) continue;
     const bool some = live[h2] && l > 0.f;
-    const float inv = some ? 1.f / (l + dif) : 0.f;
+    const float inv = some ? 1.f / rounded : 0.f;
     const long part = (long)rows[h2] * g0.n_splits + split;
 #pragma unroll
     for (int j = 0; j < kMaxND; ++j)
@@ -491,14 +518,14 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
 
 // Blocks [0, row_tiles * pre_splits): prefix items; the rest: (sequence, split) items over own
 // tokens. 128 threads.
-template <typename T>
-__global__ void __launch_bounds__(128) k_shared_mma(const shared::MmaArgs a) {
+template <typename T, int KDC>
+__global__ void __launch_bounds__(128, 3) k_shared_mma(const shared::MmaArgs a) {
   extern __shared__ __align__(16) uint8_t sm[];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
   const int n_pre = a.row_tiles * a.pre_splits, i = blockIdx.x;
   if (i < n_pre) {
-    prefix_mma_item<T>(a, i / a.pre_splits, i % a.pre_splits, sm);
+    prefix_mma_item<T, KDC>(a, i / a.pre_splits, i % a.pre_splits, sm);
   } else {
     const int j = i - n_pre;
     attn_mma_item<T, true>(a.own, j / a.own_splits, j % a.own_splits, sm);
