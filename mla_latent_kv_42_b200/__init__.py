@@ -373,42 +373,36 @@ def out_proj(dims, o_lat, w_uv, w_o, u=None, ws=None, stream=None):
     return u
 
 
-# The row and shared-prefix calls are short on the device (3 us for a decode step's rows), so their
-# host side is kept short too: one comparison per tensor decides whether it is as the call needs
-# it, and only a failed one looks closer.
+# The row and shared-prefix calls are short on the device (2 us for a decode step's rows), so their
+# host side is kept short too: one expression decides whether every tensor is as the call needs it,
+# and only a failed one looks closer.
 def _ok(t, dtype, shape, here):
     return t.dtype is dtype and t.get_device() == here and t.shape == shape and t.is_contiguous()
 
 
-def _refuse(t, name, dtype, shape, here, strided=False):
-    if t.get_device() < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != here:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous" + (" but for its rows, a multiple of 8 elements apart" if strided
-                                                     else ""))
-
-
-def _need_all(here, *named):
-    """Each (tensor, name, dtype, shape) lies on the current device, contiguous, with that type and
-    shape."""
+def _refuse(here, *named, strided=None):
+    """Raise for the first (tensor, name, dtype, shape) that is not on the current device, contiguous (but
+    for the rows of the one called ``strided``), with that type and shape."""
     for t, name, dtype, shape in named:
-        if not _ok(t, dtype, shape, here):
-            _refuse(t, name, dtype, shape, here)
+        if t.get_device() < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            if name != strided:
+                raise ValueError(f"{name} must be contiguous")
+            if t.stride(1) != 1 or t.stride(0) % 8 or t.stride(0) < shape[1]:
+                raise ValueError(f"{name} must be contiguous but for its rows, a multiple of 8 elements apart")
 
 
-def _need_rows(t, name, dtype, shape, here):
-    """The same, but the rows of ``t`` may be strided (a slice of a wider product); their distance."""
-    if _ok(t, dtype, shape, here):
-        return shape[1]
-    if (t.dtype is not dtype or t.get_device() != here or t.shape != shape or t.stride(1) != 1 or t.stride(0) % 8
-            or t.stride(0) < shape[1]):
-        _refuse(t, name, dtype, shape, here, strided=True)
-    return t.stride(0)
+def _rows_ok(t, dtype, shape, here):
+    """_ok for a tensor whose rows may be strided (a slice of a wider product)."""
+    return _ok(t, dtype, shape, here) or (t.dtype is dtype and t.get_device() == here and t.shape == shape
+                                          and t.stride(1) == 1 and t.stride(0) % 8 == 0 and t.stride(0) >= shape[1])
 
 
 def _sizes(t, n, name):
@@ -418,82 +412,85 @@ def _sizes(t, n, name):
     return t.shape
 
 
-def _current(stream):
-    """(index of the current device, stream handle)."""
-    import torch
-    here = torch.cuda.current_device()
-    return here, (torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream)
-
-
 def _pool_shape(dims, pool, fp8):
     D = dims.d_c + dims.d_rope
     n = pool.shape[0] if pool.dim() else 0
     return (n, dims.page_size * (D + 8)) if fp8 else (n, dims.page_size, D)
 
 
-def _norm_append(name, fp8, dims, x, seq_idx, pos, block_table, pool, gain_c, gain_r, eps, stream):
+def _raw_stream(torch, here, stream):
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
+
+
+def _norm_append(fn, name, fp8, dims, x, seq_idx, pos, block_table, pool, gain_c, gain_r, eps, stream):
     import torch
-    e, i32, D = _elem(dims), torch.int32, dims.d_c + dims.d_rope
-    here, st = _current(stream)
-    T = _sizes(x, 2, "x")[0]
+    e, i32 = _elem(dims), torch.int32
+    here = torch.cuda.current_device()
+    T, D = _sizes(x, 2, "x")[0], dims.d_c + dims.d_rope
     S, width = _sizes(block_table, 2, "block_table")
-    stride = _need_rows(x, "x", e, (T, D), here)
     shape = _pool_shape(dims, pool, fp8)
-    _need_all(here, (seq_idx, "seq_idx", i32, (T,)), (pos, "pos", i32, (T,)),
-              (block_table, "block_table", i32, (S, width)), (pool, "pool", torch.uint8 if fp8 else e, shape))
-    if gain_c is not None:
-        _need_all(here, (gain_c, "gain_c", e, (dims.d_c,)))
-    if gain_r is not None:
-        _need_all(here, (gain_r, "gain_r", e, (dims.d_rope,)))
-    cd = c_dims(dims)
-    _check(getattr(_lib(), name)(ctypes.byref(cd), x.data_ptr(), stride,
-                                 None if gain_c is None else gain_c.data_ptr(),
-                                 None if gain_r is None else gain_r.data_ptr(), eps, seq_idx.data_ptr(),
-                                 pos.data_ptr(), block_table.data_ptr(), S, width, pool.data_ptr(), shape[0], T, st),
-           name)
+    pool_type = torch.uint8 if fp8 else e
+    if not (_rows_ok(x, e, (T, D), here) and _ok(seq_idx, i32, (T,), here) and _ok(pos, i32, (T,), here)
+            and _ok(block_table, i32, (S, width), here) and _ok(pool, pool_type, shape, here)
+            and (gain_c is None or _ok(gain_c, e, (dims.d_c,), here))
+            and (gain_r is None or _ok(gain_r, e, (dims.d_rope,), here))):
+        _refuse(here, (x, "x", e, (T, D)), (seq_idx, "seq_idx", i32, (T,)), (pos, "pos", i32, (T,)),
+                (block_table, "block_table", i32, (S, width)), (pool, "pool", pool_type, shape),
+                *([] if gain_c is None else [(gain_c, "gain_c", e, (dims.d_c,))]),
+                *([] if gain_r is None else [(gain_r, "gain_r", e, (dims.d_rope,))]), strided="x")
+    code = fn(ctypes.byref(c_dims(dims)), x.data_ptr(), x.stride(0) if T > 1 else D,
+              None if gain_c is None else gain_c.data_ptr(), None if gain_r is None else gain_r.data_ptr(), eps,
+              seq_idx.data_ptr(), pos.data_ptr(), block_table.data_ptr(), S, width, pool.data_ptr(), shape[0], T,
+              _raw_stream(torch, here, stream))
+    if code:
+        raise MLAError(code, name)
     return pool
 
 
 def norm_append_kv(dims, x, seq_idx, pos, block_table, pool, gain_c=None, gain_r=None, eps=1e-6, stream=None):
     """mla_norm_append_kv: write rows [c ‖ k^] that the caller has (``x`` [T, d_c + d_rope], rows may be
     strided), each part RMS-normalised where its gain is given, k^ rotated, into their slots."""
-    return _norm_append("mla_norm_append_kv", False, dims, x, seq_idx, pos, block_table, pool, gain_c, gain_r, eps,
-                        stream)
+    return _norm_append(_lib().mla_norm_append_kv, "mla_norm_append_kv", False, dims, x, seq_idx, pos, block_table,
+                        pool, gain_c, gain_r, eps, stream)
 
 
 def norm_append_kv_fp8(dims, x, seq_idx, pos, block_table, pool, gain_c=None, gain_r=None, eps=1e-6, stream=None):
     """mla_norm_append_kv_fp8: the same into ``pool`` (uint8 [num_pages, fp8_page_bytes(dims)])."""
-    return _norm_append("mla_norm_append_kv_fp8", True, dims, x, seq_idx, pos, block_table, pool, gain_c, gain_r, eps,
-                        stream)
+    return _norm_append(_lib().mla_norm_append_kv_fp8, "mla_norm_append_kv_fp8", True, dims, x, seq_idx, pos,
+                        block_table, pool, gain_c, gain_r, eps, stream)
 
 
-def _read(name, fp8, dims, pool, seq_idx, pos, block_table, out, stream):
+def _read(fn, name, fp8, dims, pool, seq_idx, pos, block_table, out, stream):
     import torch
-    e, i32, D = _elem(dims), torch.int32, dims.d_c + dims.d_rope
-    here, st = _current(stream)
-    T = _sizes(seq_idx, 1, "seq_idx")[0]
+    e, i32 = _elem(dims), torch.int32
+    here = torch.cuda.current_device()
+    T, D = _sizes(seq_idx, 1, "seq_idx")[0], dims.d_c + dims.d_rope
     S, width = _sizes(block_table, 2, "block_table")
     shape = _pool_shape(dims, pool, fp8)
-    _need_all(here, (pool, "pool", torch.uint8 if fp8 else e, shape), (seq_idx, "seq_idx", i32, (T,)),
-              (pos, "pos", i32, (T,)), (block_table, "block_table", i32, (S, width)))
+    pool_type = torch.uint8 if fp8 else e
+    if not (_ok(pool, pool_type, shape, here) and _ok(seq_idx, i32, (T,), here) and _ok(pos, i32, (T,), here)
+            and _ok(block_table, i32, (S, width), here) and (out is None or _rows_ok(out, e, (T, D), here))):
+        _refuse(here, (pool, "pool", pool_type, shape), (seq_idx, "seq_idx", i32, (T,)), (pos, "pos", i32, (T,)),
+                (block_table, "block_table", i32, (S, width)),
+                *([] if out is None else [(out, "out", e, (T, D))]), strided="out")
     if out is None:
-        out, stride = pool.new_empty((T, D), dtype=e), D
-    else:
-        stride = _need_rows(out, "out", e, (T, D), here)
-    cd = c_dims(dims)
-    _check(getattr(_lib(), name)(ctypes.byref(cd), pool.data_ptr(), shape[0], seq_idx.data_ptr(), pos.data_ptr(),
-                                 block_table.data_ptr(), S, width, out.data_ptr(), stride, T, st), name)
+        out = pool.new_empty((T, D), dtype=e)
+    code = fn(ctypes.byref(c_dims(dims)), pool.data_ptr(), shape[0], seq_idx.data_ptr(), pos.data_ptr(),
+              block_table.data_ptr(), S, width, out.data_ptr(), out.stride(0) if T > 1 else D, T,
+              _raw_stream(torch, here, stream))
+    if code:
+        raise MLAError(code, name)
     return out
 
 
 def read_kv(dims, pool, seq_idx, pos, block_table, out=None, stream=None):
     """mla_read_kv: the cached rows of the given (sequence, position) pairs, [T, d_c + d_rope]."""
-    return _read("mla_read_kv", False, dims, pool, seq_idx, pos, block_table, out, stream)
+    return _read(_lib().mla_read_kv, "mla_read_kv", False, dims, pool, seq_idx, pos, block_table, out, stream)
 
 
 def read_kv_fp8(dims, pool, seq_idx, pos, block_table, out=None, stream=None):
     """mla_read_kv_fp8: the same from an FP8 cache, as element-type rows."""
-    return _read("mla_read_kv_fp8", True, dims, pool, seq_idx, pos, block_table, out, stream)
+    return _read(_lib().mla_read_kv_fp8, "mla_read_kv_fp8", True, dims, pool, seq_idx, pos, block_table, out, stream)
 
 
 def shared_prefix_attention(dims, q, pool, block_table, seq_lens, max_seq_len, shared_pages, o_lat=None, lse=None,
@@ -502,33 +499,35 @@ def shared_prefix_attention(dims, q, pool, block_table, seq_lens, max_seq_len, s
     ``shared_pages`` (int32 [num_shared_pages], all full), which are attended once for the batch."""
     import torch
     e, i32, H = _elem(dims), torch.int32, dims.n_heads
-    here, st = _current(stream)
+    here = torch.cuda.current_device()
     B = _sizes(q, 3, "q")[0]
     width = _sizes(block_table, 2, "block_table")[1]
     n_shared = _sizes(shared_pages, 1, "shared_pages")[0]
-    shape = _pool_shape(dims, pool, False)
-    _need_all(here, (q, "q", e, (B, H, dims.d_c + dims.d_rope)), (pool, "pool", e, shape),
-              (block_table, "block_table", i32, (B, width)), (seq_lens, "seq_lens", i32, (B,)),
-              (shared_pages, "shared_pages", i32, (n_shared,)))
+    shape, q_shape = _pool_shape(dims, pool, False), (B, H, dims.d_c + dims.d_rope)
+    if not (_ok(q, e, q_shape, here) and _ok(pool, e, shape, here) and _ok(block_table, i32, (B, width), here)
+            and _ok(seq_lens, i32, (B,), here) and _ok(shared_pages, i32, (n_shared,), here)
+            and (o_lat is None or _ok(o_lat, e, (B, H, dims.d_c), here))
+            and (lse is None or _ok(lse, torch.float32, (B, H), here))
+            and (ws is None or ws.is_contiguous() and ws.get_device() == here)):
+        _refuse(here, (q, "q", e, q_shape), (pool, "pool", e, shape), (block_table, "block_table", i32, (B, width)),
+                (seq_lens, "seq_lens", i32, (B,)), (shared_pages, "shared_pages", i32, (n_shared,)),
+                *([] if o_lat is None else [(o_lat, "o_lat", e, (B, H, dims.d_c))]),
+                *([] if lse is None else [(lse, "lse", torch.float32, (B, H))]),
+                *([] if ws is None else [(ws, "ws", ws.dtype, ws.shape)]))
     if o_lat is None:
         o_lat = q.new_empty((B, H, dims.d_c))
-    else:
-        _need_all(here, (o_lat, "o_lat", e, (B, H, dims.d_c)))
-    if lse is not None:
-        _need_all(here, (lse, "lse", torch.float32, (B, H)))
-    elif want_lse:
+    if lse is None and want_lse:
         lse = q.new_empty((B, H), dtype=torch.float32)
-    cd = c_dims(dims)
-    lib = _lib()
+    lib, cd = _lib(), ctypes.byref(c_dims(dims))
     if ws is None:
-        ws = q.new_empty(max(lib.mla_workspace_size(ctypes.byref(cd), CALL_SHARED_PREFIX_ATTENTION, B, max_seq_len),
-                             16), dtype=torch.uint8)
-    elif not ws.is_contiguous() or ws.get_device() != here:
-        raise ValueError(f"ws must be contiguous and on the current device, cuda:{here}")
-    _check(lib.mla_shared_prefix_attention(
-        ctypes.byref(cd), q.data_ptr(), pool.data_ptr(), shape[0], block_table.data_ptr(), width, seq_lens.data_ptr(),
-        B, max_seq_len, shared_pages.data_ptr(), n_shared, o_lat.data_ptr(), None if lse is None else lse.data_ptr(),
-        ws.data_ptr(), ws.nbytes, st), "mla_shared_prefix_attention")
+        n = lib.mla_workspace_size(cd, CALL_SHARED_PREFIX_ATTENTION, B, max_seq_len)
+        ws = q.new_empty(max(n, 16), dtype=torch.uint8)
+    code = lib.mla_shared_prefix_attention(
+        cd, q.data_ptr(), pool.data_ptr(), shape[0], block_table.data_ptr(), width, seq_lens.data_ptr(), B,
+        max_seq_len, shared_pages.data_ptr(), n_shared, o_lat.data_ptr(), None if lse is None else lse.data_ptr(),
+        ws.data_ptr(), ws.nbytes, _raw_stream(torch, here, stream))
+    if code:
+        raise MLAError(code, "mla_shared_prefix_attention")
     return o_lat, lse
 
 

@@ -139,7 +139,9 @@ struct DecodeTcMaps {
 // the whole sequence and an item that one pair finishes goes straight to o_lat; with them every
 // result is an fp32 partial.
 struct SharedTcMaps : DecodeTcMaps {
-  CUtensorMap o_pre, o_pre_h;  // partials of the prefix items: (512 columns, 128 rows, items + C)
+  // partials of the prefix items: (512 columns, 128 rows, items + C). o_pre, o_part and o_lat have
+  // boxes of 128 bytes x 32 rows here, in the 128-byte swizzle.
+  CUtensorMap o_pre, o_pre_h;
   CUtensorMap q1;              // queries with boxes of one chunk x own_q_rows rows (own_q_rows > 0)
 };
 // A pair spends on an item, beside its tiles, the time of about kItemUnits more: its queries'
@@ -150,7 +152,7 @@ constexpr int kItemUnits = 2;
 struct SharedTcParams : DecodeTcParams {
   const int* first;         // [B], -1 for a rejected sequence (which has no tiles)
   const int* shared_pages;  // pages of the prefix
-  const int* start;         // [C] item that each pair begins in
+  const int4* start;        // [C] item that each pair begins in, its places [y, z), all places
   int prefix_items, prefix_len;
   int own_q_rows;           // n_h rounded up to 8 where a sequence's rows fit one small box, else 0
   float* lse_pre;           // [items + C][128]
@@ -163,6 +165,7 @@ struct Item {
 struct ItemIter {
   long g, g_end;
   int b;
+  int base, next;  // kShared: places [base, next) of item b
 };
 
 __device__ __forceinline__ ItemIter item_iter(const int* prefix, int B, int cluster, int nclusters) {
@@ -178,27 +181,43 @@ __device__ __forceinline__ ItemIter item_iter(const int* prefix, int B, int clus
   it.b = lo;
   return it;
 }
-// The same with the item that the range begins in given.
-__device__ __forceinline__ ItemIter item_iter_at(const int* prefix, int B, int cluster, int nclusters, int b) {
-  const long T = prefix[B];
-  return ItemIter{T * cluster / nclusters, T * (cluster + 1) / nclusters, b};
+// The same with the item that the range begins in given, as the shared-prefix plan writes it for each
+// pair: (item, its first place, its last + 1, all places).
+__device__ __forceinline__ ItemIter item_iter_at(const int4& at, int cluster, int nclusters) {
+  const long T = at.w;
+  return ItemIter{T * cluster / nclusters, T * (cluster + 1) / nclusters, at.x, at.y, at.z};
 }
 // kUnits: places an item takes in the list before its tiles, for its share of the split (kItemUnits
 // below); 0 where the list holds tiles alone.
 template <int kUnits>
 __device__ __forceinline__ bool next_item(ItemIter& it, const int* prefix, Item& out) {
-  while (it.g < it.g_end) {
+  if constexpr (kUnits == 0) {
+    if (it.g >= it.g_end) return false;
     while (prefix[it.b + 1] <= it.g) ++it.b;
-    const int base = prefix[it.b] + kUnits;
+    const int base = prefix[it.b];
     out.b = it.b;
     out.n_b = prefix[it.b + 1] - base;
-    out.t0 = max(0, (int)(it.g - base));
-    const long end = min(it.g_end, (long)prefix[it.b + 1]);
-    out.t1 = (int)(end - base);
-    it.g = end;
-    if (kUnits == 0 || out.t1 > out.t0) return true;
+    out.t0 = (int)(it.g - base);
+    out.t1 = (int)(min(it.g_end, (long)prefix[it.b + 1]) - base);
+    it.g = base + out.t1;
+    return true;
+  } else {
+    while (it.g < it.g_end) {
+      while (it.next <= it.g) {
+        it.base = it.next;
+        it.next = prefix[++it.b + 1];
+      }
+      const int base = it.base + kUnits;
+      const long end = min(it.g_end, (long)it.next);
+      out.b = it.b;
+      out.n_b = it.next - base;
+      out.t0 = max(0, (int)(it.g - base));
+      out.t1 = (int)(end - base);
+      it.g = end;
+      if (out.t1 > out.t0) return true;  // not the places before the tiles alone
+    }
+    return false;
   }
-  return false;
 }
 
 // The pair's tiles in order. Every role walks the same sequence with a cursor of its own:
@@ -210,10 +229,9 @@ struct CursorOf {
   Item item;
   int t, ti, ii;
   bool valid;
-  __device__ __forceinline__ void start(const int* prefix, int B, int cluster, int nclusters,
-                                        const int* starts = nullptr) {
-    it = starts != nullptr ? item_iter_at(prefix, B, cluster, nclusters, starts[cluster])
-                           : item_iter(prefix, B, cluster, nclusters);
+  __device__ __forceinline__ void start(const int* prefix, int B, int cluster, int nclusters, const int4& at) {
+    if constexpr (kUnits == 0) it = item_iter(prefix, B, cluster, nclusters);
+    else it = item_iter_at(at, cluster, nclusters);
     valid = next_item<kUnits>(it, prefix, item);
     t = valid ? item.t0 : 0;
     ti = 0;
@@ -356,8 +374,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
   if (threadIdx.x == 0) griddep_launch();
   griddep_wait();  // the plan, the query and the cache come from earlier kernels
   const int* prefix = p.tile_prefix;
+  int4 start_at = make_int4(0, 0, 0, 0);
+  if constexpr (kShared) start_at = p.start[cluster];
   const bool has_work = [&] {
-    const long T_ = prefix[p.B];
+    const long T_ = kShared ? start_at.w : prefix[p.B];
     return T_ * (cluster + 1) / nclusters > T_ * cluster / nclusters;
   }();
   const uint32_t peer_abort = mapa(smem_u32(&ctl->abort_flag), rank ^ 1u);
@@ -375,8 +395,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
     return ok;
   };
   const uint32_t set_u32 = data_u32 + kSetOff;
-  const int* starts = nullptr;
-  if constexpr (kShared) starts = p.start;
   // Item b's tokens, pages and first query row: sequence b itself, or (kShared) 128 packed rows
   // over the shared pages or a sequence's own tokens.
   auto item_len = [&](int b) {
@@ -421,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         }
         tma_prefetch_map(&maps.q9);
         Cursor c;
-        c.start(prefix, p.B, cluster, nclusters, starts);
+        c.start(prefix, p.B, cluster, nclusters, start_at);
         int L = 0;
         const int* btb = nullptr;
         while (c.valid) {
@@ -497,7 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
       // done with the own page's columns in those slots (a tail page with its zero-filled rows).
       if (lane == 0) {
         Cursor c;
-        c.start(prefix, p.B, cluster, nclusters, starts);
+        c.start(prefix, p.B, cluster, nclusters, start_at);
         int L = 0;
         const int* btb = nullptr;
         const int g = 1 - (int)rank;
@@ -562,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
           return false;
         };
         Cursor c;
-        c.start(prefix, p.B, cluster, nclusters, starts);
+        c.start(prefix, p.B, cluster, nclusters, start_at);
         if (warp == kMmaWarp) {
           // S(i) = Q C^T into S buffer i & 1
           const uint32_t q_lo = desc_sw128_lo(data_u32 + kQOff, 16);
@@ -781,7 +799,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
       };
       if constexpr (F8) {
         Cursor c;
-        c.start(prefix, p.B, cluster, nclusters, starts);
+        c.start(prefix, p.B, cluster, nclusters, start_at);
         int L = c.valid ? p.seq_lens[c.item.b] : 0;
         TileScales cur = c.valid ? tile_scales(c, L) : TileScales{};
         while (c.valid) {
@@ -845,7 +863,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         return true;
       };
       Cursor c;
-      c.start(prefix, p.B, cluster, nclusters, starts);
+      c.start(prefix, p.B, cluster, nclusters, start_at);
       float m_ref = -INFINITY, lsum = 0.f;
       float ldif = 0.f;  // kShared: what the rounding of the weights adds to their sum
       int L = 0;
@@ -919,9 +937,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         // P row h, tokens [32ch, 32ch + 32) of page g: p = 2^(s * scale - m_ref), one FFMA and one
         // ex2 per token. The sum of the rounded weights is the denominator (it matches what the
         // MMA accumulates). kShared sums the weights before rounding for the lse, which so is good
-        // to fp32 (rounded weights shift it by up to 2^-9), and what rounding adds for the denominator.
+        // to fp32 (rounded weights shift it by up to 2^-9), and what rounding adds for the
+        // denominator, both once P is handed over, so that the O MMAs do not wait for them.
         float sums[4] = {0.f, 0.f, 0.f, 0.f};
-        float difs[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t packed_w[kShared ? 16 : 1];
 #pragma unroll
         for (int u4 = 0; u4 < 4; ++u4) {
           uint32_t w[4];
@@ -931,23 +950,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
             const float w0 = ex2_approx(fmaf(u2f(sr[k]), p.scale_log2, -m_ref));
             const float w1 = ex2_approx(fmaf(u2f(sr[k + 1]), p.scale_log2, -m_ref));
             const typename Pack<PT>::T2 pr2 = Pack<PT>::make(w0, w1);
-            const float2 back = Pack<PT>::f2(pr2);
+            w[e] = *reinterpret_cast<const uint32_t*>(&pr2);
             if constexpr (kShared) {
-              sums[e] += w0 + w1;
-              difs[e] += (back.x - w0) + (back.y - w1);
+              sr[k] = __float_as_uint(w0);
+              sr[k + 1] = __float_as_uint(w1);
+              packed_w[4 * u4 + e] = w[e];
             } else {
+              const float2 back = Pack<PT>::f2(pr2);
               sums[e] += back.x + back.y;
             }
-            w[e] = *reinterpret_cast<const uint32_t*>(&pr2);
           }
           *reinterpret_cast<uint4*>(p_row_ptr + ((((4 * ch + u4) ^ (h & 7))) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        lsum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-        if constexpr (kShared) ldif += (difs[0] + difs[1]) + (difs[2] + difs[3]);
+        if constexpr (!kShared) lsum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         fence_proxy_async_cta();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cl(lead(ctl->p_full));
+        if constexpr (kShared) {
+          float difs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float w0 = u2f(sr[2 * k]), w1 = u2f(sr[2 * k + 1]);
+            const float2 back = Pack<PT>::f2(*reinterpret_cast<const typename Pack<PT>::T2*>(&packed_w[k]));
+            sums[k & 3] += w0 + w1;
+            difs[k & 3] += (back.x - w0) + (back.y - w1);
+          }
+          lsum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+          ldif += (difs[0] + difs[1]) + (difs[2] + difs[3]);
+        }
 
         if (c.last()) {  // ---- epilogue of the item: O / l for this thread's head and columns
           if (!wwait(ctl->p_free, ti & 1)) break;  // the last O MMAs are done
@@ -1057,6 +1088,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
                     *reinterpret_cast<float4*>(dst + c0 + e) =
                         make_float4(u2f(r[e]) * inv, u2f(r[e + 1]) * inv, u2f(r[e + 2]) * inv, u2f(r[e + 3]) * inv);
                 }
+              }
+            }
+          }
+          if constexpr (kShared) {
+            // The pair's last item: the warp's 32 rows x 128 columns all go to the 16 KB it has in
+            // the free latent sets, in boxes of 128 bytes a row, under one fence and one wait (the
+            // rounds below have a fence each: 3.2 us for a partial against 1.7).
+            if (last_item && c_end > 0) {
+              c_end = 0;
+              const uint32_t stage_u32 = set_u32 + warp * 16384;
+              uint8_t* const stage = data + (stage_u32 - data_u32) + lane * 128;
+              const int sw = lane & 7;
+#pragma unroll
+              for (int c0 = 0; c0 < 128; c0 += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + lane_base + kOCol + 128 * ch + c0, r);
+                tmem_wait_ld();
+                if (whole) {  // 32 columns: half a 128-byte row
+                  uint8_t* const box = stage + (c0 / 64) * 4096;
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      const typename Pack<T>::T2 v =
+                          Pack<T>::make(u2f(r[8 * u + 2 * e]) * inv, u2f(r[8 * u + 2 * e + 1]) * inv);
+                      w[e] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    *reinterpret_cast<uint4*>(box + (((c0 / 8 % 8 + u) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                  }
+                } else {
+                  uint8_t* const box = stage + (c0 / 32) * 4096;
+#pragma unroll
+                  for (int u = 0; u < 8; ++u)
+                    *reinterpret_cast<float4*>(box + ((u ^ sw) << 4)) =
+                        make_float4(u2f(r[4 * u]) * inv, u2f(r[4 * u + 1]) * inv, u2f(r[4 * u + 2]) * inv,
+                                    u2f(r[4 * u + 3]) * inv);
+                }
+              }
+              fence_proxy_async_cta();
+              __syncwarp();
+              if (lane == 0) {
+                if (whole) {
+                  for (int k = 0; k < 2; ++k) tma_store_3d(&maps.o_lat, stage_u32 + 4096 * k, col0 + 64 * k, head0, ib);
+                } else {
+                  for (int k = 0; k < 4; ++k) tma_store_3d(part_map, stage_u32 + 4096 * k, col0 + 32 * k, head0, (int)slot);
+                }
+                bulk_commit_group();
               }
             }
           }

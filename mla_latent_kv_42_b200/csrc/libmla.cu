@@ -565,7 +565,7 @@ SharedTcLayout shared_tc_layout(const mla_dims* d, int B, bool packed) {
   L.len = take((size_t)B * 4);
   L.tile_prefix = take(((size_t)L.Mt + B + 1) * 4);
   L.pairs = take(((size_t)L.Mt + B) * 4);
-  L.start = take(C * 4);
+  L.start = take(C * sizeof(int4));
   L.o_pre = take(pre_rows * tc::dec::kDc * 4);
   L.lse_pre = take(pre_rows * 4);
   L.o_part = take(own_rows * tc::dec::kDc * 4);
@@ -616,7 +616,7 @@ size_t ws_shared(const mla_dims* d, int B, int max_seq_len) {
 
 // Rows up to which the merge gives a row four groups of threads: two row tiles over 74 pairs are cut
 // into 37 parts each, one into 74.
-constexpr unsigned kMergeFewRows = 256;
+constexpr unsigned kMergeFewRows = 256, kMergeManyRows = 2048;
 
 template <typename T>
 int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_pages, shared::PlanArgs& plan,
@@ -629,7 +629,7 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   plan.len = reinterpret_cast<int*>(ws + L.len);
   plan.tile_prefix = reinterpret_cast<int*>(ws + L.tile_prefix);
   plan.pairs = reinterpret_cast<int*>(ws + L.pairs);
-  plan.start = reinterpret_cast<int*>(ws + L.start);
+  plan.start = reinterpret_cast<int4*>(ws + L.start);
   plan.C = C;
   float* o_pre = reinterpret_cast<float*>(ws + L.o_pre);
   float* o_part = reinterpret_cast<float*>(ws + L.o_part);
@@ -642,13 +642,13 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
             host::encode_pages(&maps.page2, pool, bf16, (uint64_t)num_pages, tc::dec::kD * 2, 2) &&
             host::encode_pages(&maps.page4, pool, bf16, (uint64_t)num_pages, tc::dec::kD * 2, 4) &&
             host::encode_chunks(&maps.q9, q, bf16, (uint64_t)B * n_h, tc::dec::kD * 2, 9) &&
-            host::encode_heads_out(&maps.o_part, o_part, f32, 4, (uint64_t)n_h, (uint64_t)B + C) &&
+            host::encode_heads_out(&maps.o_part, o_part, f32, 4, (uint64_t)n_h, (uint64_t)B + C, true) &&
             host::encode_heads_out32(&maps.o_part_h, o_part, f32, 4, (uint64_t)n_h, (uint64_t)B + C);
   if (L.Mt > 0)
-    ok = ok && host::encode_heads_out(&maps.o_pre, o_pre, f32, 4, 128, (uint64_t)L.Mt + C) &&
+    ok = ok && host::encode_heads_out(&maps.o_pre, o_pre, f32, 4, 128, (uint64_t)L.Mt + C, true) &&
          host::encode_heads_out32(&maps.o_pre_h, o_pre, f32, 4, 128, (uint64_t)L.Mt + C);
   else
-    ok = ok && host::encode_heads_out(&maps.o_lat, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B) &&
+    ok = ok && host::encode_heads_out(&maps.o_lat, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B, true) &&
          host::encode_heads_out32(&maps.o_lat_h, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B);
   // a sequence's own item of at most 32 heads loads its own query rows, 8 at least, chunk by chunk
   const int own_q_rows = L.Mt > 0 && n_h <= 32 ? (n_h + 7) / 8 * 8 : 0;
@@ -682,9 +682,12 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   const shared::MergeArgs m{o_pre, p.lse_pre, o_part, p.lse_part, plan.tile_prefix, plan.pairs, plan.first, B, n_h,
                             L.Mt, C, o_lat, lse_out};
   const unsigned R = (unsigned)((long)B * n_h);
-  const cudaError_t e = R <= kMergeFewRows ? launch_pdl(k_shared_merge<T, 128, 4>, dim3(R), dim3(512), 0, st, m)
-                                           : launch_pdl(k_shared_merge<T, 64, 1>, dim3((R + shared::kMergeRows - 1) / shared::kMergeRows),
-                                                        dim3(64 * shared::kMergeRows), 0, st, m);
+  // 128-thread blocks of two rows, or of four where rows fill the SMs several times over (8192 rows
+  // of two to four parts: 8.8 us with a warp to a row, 12.1 with two; 1024 rows of eleven: 6.2, 5.8)
+  const cudaError_t e =
+      R <= kMergeFewRows    ? launch_pdl(k_shared_merge<T, 128, 4>, dim3(R), dim3(512), 0, st, m)
+      : R <= kMergeManyRows ? launch_pdl(k_shared_merge<T, 64, 1>, dim3((R + 1) / 2), dim3(128), 0, st, m)
+                            : launch_pdl(k_shared_merge<T, 32, 1>, dim3((R + 3) / 4), dim3(128), 0, st, m);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   launches += 3;
   return MLA_OK;

@@ -31,7 +31,7 @@ struct PlanArgs {
   int* tile_prefix;  // [prefix_items + B + 1] places before each item in the list of the items'
                      // tiles, kItemUnits places and then its tiles to an item that has any; or null
   int* pairs;        // [prefix_items + B] first and last pair of an item's tiles, c0 | c1 << 16, -1: none
-  int* start;        // [C] item that each pair begins in
+  int4* start;       // [C] item that each pair begins in, its places [y, z), all places
   int C;             // pairs
 };
 }  // namespace shared
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
   };
   for (int i = tid; i < a.prefix_items; i += 1024) a.pairs[i] = pairs_of(i * nt, nt);
   s_run[tid] = a.prefix_items * nt + incl - sum + (warp > 0 ? warp_total[warp - 1] : 0);
-  int run = a.prefix_items * nt + incl - sum + (warp > 0 ? warp_total[warp - 1] : 0);
+  int run = s_run[tid];
   for (int b = b0; b < b1; ++b) {
     const int n = count[b];  // read before the same place may be overwritten
     mine[b] = run;
@@ -143,20 +143,34 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
   }
   if (tid == 1023) mine[a.B] = (int)T;
   __syncthreads();
-  if (tid < a.C) {  // the item that pair tid begins in, or one before it whose places end there
-    const int g = (int)(T * tid / a.C);
+  if (tid < a.C) {                  // the item that pair tid begins in
+    const int g = narrow ? (int)((unsigned)T * (unsigned)tid / (unsigned)a.C) : (int)(T * tid / a.C);
+    int item, base, next;
     if (g < a.prefix_items * nt) {
-      a.start[tid] = g / nt;
+      item = g / nt;
+      base = item * nt;
+      next = base + nt;
     } else {
       int lo = 0, hi = 1023;  // the last thread whose sequences begin at or before g
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (s_run[mid] <= g) lo = mid; else hi = mid - 1;
       }
+      // (threads past the last sequence hold the total, which only a list without places reaches)
       int b = min(lo * per, a.B - 1);
-      while (b + 1 < a.B && mine[b + 1] <= g) ++b;
-      a.start[tid] = a.prefix_items + b;
+      base = s_run[lo];
+      if (per == 1) {
+        next = b + 1 < a.B ? s_run[b + 1] : (int)T;
+      } else {
+        while (b + 1 < a.B && (next = mine[b + 1]) <= g) {
+          ++b;
+          base = next;
+        }
+        if (b + 1 == a.B) next = (int)T;
+      }
+      item = a.prefix_items + b;
     }
+    a.start[tid] = make_int4(item, base, next, (int)T);
   }
 }
 
@@ -190,18 +204,18 @@ struct Parts {
     return kDense ? first + k : item + ((g0 + k + 1) * C - 1) / T;
   }
 };
-constexpr int kMergeAhead = 8;  // parts a thread has in flight (four where it has two vectors of each)
-constexpr int kMergeRows = 4;   // rows of a block whose rows have one group each
+constexpr int kMergeAhead = 8;  // vectors of parts that a thread has in flight
 }  // namespace shared
 
 // Joins each query row's partials, those over the prefix and those over its own tokens, in a fixed
 // order. kGroups groups of kLanes threads share a row and take its parts in turn, a thread 512 /
-// kLanes of the latent values and kMergeAhead parts in flight: four groups where the rows are few
-// and so are cut into many parts, one of fewer threads where they are many (at 8192 rows of two
-// parts the instructions of 128 threads a row took longer than the partials' bytes). Every warp
-// forms the weights of up to 32 parts for itself; more go through shared memory where a block has one
-// row. A rejected sequence gets zeros and an lse of -inf. Without prefix items a row that one pair
-// finished is already in o_lat. A block of four groups has one row, else kMergeRows of them.
+// kLanes of the latent values and kMergeAhead vectors of parts in flight: four groups where the
+// rows are few and so are cut into many parts, one of fewer threads where they are many (at 8192
+// rows of two parts the instructions of 128 threads a row took longer than the partials' bytes).
+// Every warp forms the weights of up to 32 parts for itself; more go through shared memory where a
+// block has one row. A rejected sequence gets zeros and an lse of -inf. Without prefix items a row
+// that one pair finished is already in o_lat. A block of four groups has one row, else its 128
+// threads have 128 / kLanes.
 template <typename T, int kLanes, int kGroups, bool kDense>
 __device__ __forceinline__ void merge_row(const shared::MergeArgs& a, const shared::Parts& pp, const shared::Parts& po,
                                           int r, int b, int T_) {
@@ -307,9 +321,8 @@ __device__ __forceinline__ void merge_row(const shared::MergeArgs& a, const shar
 }
 
 template <typename T, int kLanes, int kGroups>
-__global__ void __launch_bounds__(kLanes* kGroups * (kGroups > 1 ? 1 : shared::kMergeRows))
-    k_shared_merge(const shared::MergeArgs a) {
-  constexpr int kThreads = kLanes * kGroups, kRows = kGroups > 1 ? 1 : shared::kMergeRows;
+__global__ void __launch_bounds__(kGroups > 1 ? kLanes * kGroups : 128) k_shared_merge(const shared::MergeArgs a) {
+  constexpr int kThreads = kLanes * kGroups, kRows = kGroups > 1 ? 1 : 128 / kLanes;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
   const int r = (int)blockIdx.x * kRows + (int)threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
