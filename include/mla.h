@@ -345,8 +345,8 @@ int mla_read_kv_fp8(const mla_dims* dims, const void* pool, int32_t num_pages, c
  * sequence at least that long begins with these pages, and its block-table row lists them too (the
  * call reads them from either place). A sequence that is shorter, such as an idle row of a padded
  * batch, attends to the seq_lens[b] tokens of its own row alone.
- * The other arguments, limits and outputs as mla_decode_attention; twice the pages of B sequences
- * of max_seq_len must stay below 2^31. lse_out is good to fp32 where d_c = 512, d_rope = 64 and
+ * The other arguments, limits and outputs as mla_decode_attention; 2 B (pages of max_seq_len + 2)
+ * must stay below 2^31. lse_out is good to fp32 where d_c = 512, d_rope = 64 and
  * page_size = 64 or where the shape meets mla_layer_step_small's limits on heads, widths and pages:
  * those are the shapes with kernels of their own (any head count at the first). Other shapes run as
  * mla_decode_attention does. A bad length or page id zeroes that sequence's output (lse -inf) and

@@ -49,10 +49,12 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
   if (threadIdx.x == 0) griddep_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = a.page_size, shared_len = a.n_shared * P;
-  // the first sequence's length is requested beside the shared pages
+  // the first sequence's length, and the page it then most likely asks for first, are requested
+  // beside the shared pages
   const int per_pass = 1024 / a.lanes, sub = tid & (a.lanes - 1);
-  const int b_first = tid / a.lanes;
+  const int b_first = tid / a.lanes, t_first = a.n_shared + sub;
   const int L_first = b_first < a.B ? a.seq_lens[b_first] : 0;
+  const int pg_first = b_first < a.B && t_first < a.max_pages ? a.bt[(long)b_first * a.max_pages + t_first] : 0;
   bool bad = false;
   for (int t = tid; t < a.n_shared; t += 1024) {
     const int pg = a.shared_pages[t];
@@ -66,15 +68,20 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) 
     if (b < a.B) {
       L = b0 == 0 ? L_first : a.seq_lens[b];
       len_ok = L >= 1 && L <= a.max_seq_len;
-      n = len_ok ? (L + P - 1) / P : 0;
+      n = len_ok ? (L - 1) / P + 1 : 0;
       len_ok = len_ok && n <= a.max_pages;
       f = len_ok && shared_len > 0 && L >= shared_len ? shared_len : 0;
     }
     bad = false;
     if (len_ok) {
       const int* row = a.bt + (long)b * a.max_pages;
+      int t = f / P + sub;
+      if (b0 == 0 && t == t_first && t < n) {
+        bad |= pg_first < 0 || pg_first >= a.num_pages;
+        t += a.lanes;
+      }
 #pragma unroll 4
-      for (int t = f / P + sub; t < n; t += a.lanes) {
+      for (; t < n; t += a.lanes) {
         const int pg = row[t];
         bad |= pg < 0 || pg >= a.num_pages;
       }
