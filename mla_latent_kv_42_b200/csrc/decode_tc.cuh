@@ -87,7 +87,7 @@ struct Ctrl {
   uint64_t s_full[2], p_free;
   // Local barriers.
   uint64_t mx_full[2][2];  // exchanges among the softmax warps: [head group][buffer xm, xh]
-  uint64_t staged;         // an item's epilogue boxes in P have been read, by all 8 softmax warps
+  uint64_t staged;         // kShared: all 8 softmax warps are through an item's epilogue
   uint64_t f8_qk[2][2], f8_pv[2][2], f8_rope;  // FP8: an e4m3 box has landed in this CTA
   uint64_t f8_q;                               // FP8: this CTA's queries have landed
   uint64_t drain;
@@ -139,9 +139,7 @@ struct DecodeTcMaps {
 // the whole sequence and an item that one pair finishes goes straight to o_lat; with them every
 // result is an fp32 partial.
 struct SharedTcMaps : DecodeTcMaps {
-  // partials of the prefix items: (512 columns, 128 rows, items + C). o_pre, o_part and o_lat have
-  // boxes of 128 bytes x 32 rows here, in the 128-byte swizzle.
-  CUtensorMap o_pre, o_pre_h;
+  CUtensorMap o_pre, o_pre_h;  // partials of the prefix items: (512 columns, 128 rows, items + C)
   CUtensorMap q1;              // queries with boxes of one chunk x own_q_rows rows (own_q_rows > 0)
 };
 // A pair spends on an item, beside its tiles, the time of about kItemUnits more: its queries'
@@ -895,8 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         for (int k = 0; k < 8; ++k) mxs[k] = u2f(sr[k]);
 #pragma unroll
         for (int k = 8; k < 32; ++k) mxs[k & 7] = fmaxf(mxs[k & 7], u2f(sr[k]));
-        // a new item: the other warps' epilogue boxes, which lie in P rows of any warp, have left,
-        // and (kShared) both exchange buffers have been read
+        // kShared: both exchange buffers have been read at the end of the item before
         if (kShared && c.first() && c.ii > 0 && !wwait(ctl->staged, (c.ii - 1) & 1)) break;
         float four[4];
         if (!exchange(fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
@@ -914,7 +911,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
         }
         // the O MMAs of the previous tile are done: P may be overwritten and O rescaled
         if (!wwait(ctl->p_free, (ti & 1) ^ 1)) break;
-        if (!kShared && c.first() && c.ii > 0 && !wwait(ctl->staged, (c.ii - 1) & 1)) break;
         if (!c.first() && __any_sync(0xffffffffu, alpha != 1.f)) {
           tc_fence_after();
           // two TMEM loads in flight per wait (one with the FP8 cache's smaller register budget)
@@ -1013,10 +1009,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
           // shared memory: each lane puts its head's segment in row `lane` of a 2 KB box in the
           // 64-byte swizzle (16-byte chunk c of row r at c ^ (r/2 % 4), conflict-free), and lane 0
           // stores the 32 x 64-byte box with one TMA store, which heads past n_h fall outside of.
-          // Mid-range the warp's 2 KB of the P buffer (free: the last O MMAs are done) holds two
-          // 1 KB boxes of 32 bytes per head, used in turn by half rounds, so a box waits only for
-          // the store two half rounds back; at the pair's last item every round gets a 2 KB box
-          // of its own in the latent sets, which no tile needs any more, so nothing waits.
+          // Mid-range 2 KB of the P buffer (free: the last O MMAs are done) hold two 1 KB boxes of
+          // 32 bytes per head, used in turn by half rounds, so a box waits only for the store two
+          // half rounds back. They are P rows that the warps of this exchange group write: a
+          // group's next P comes after its next exchange, which every warp of it enters with its
+          // stores read, while the other group may be ahead or behind. At the pair's last item
+          // every round gets a 2 KB box of its own in the latent sets, which no tile needs any
+          // more, so nothing waits.
           const bool last_item = c.it.g >= c.it.g_end;
           const uint32_t wsw = (lane >> 1) & 3;
           const int head0 = 64 * (int)rank + 32 * (qd & 1);
@@ -1034,7 +1033,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
               // of P (unswizzled), each box reused once the store two half rounds back has read it
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t box_u32 = data_u32 + kPOff + warp * 2048 + (round & 1) * 1024;
+                const uint32_t box_u32 = data_u32 + kPOff + (warp >> 2) * kChunk + xg * 4096 + ((warp >> 1) & 1) * 2048 +
+                                         (round & 1) * 1024;
                 uint8_t* const box = data + (box_u32 - data_u32);
                 ++round;
                 if (lane == 0) bulk_wait_read<1>();
@@ -1091,54 +1091,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
               }
             }
           }
-          if constexpr (kShared) {
-            // The pair's last item: the warp's 32 rows x 128 columns all go to the 16 KB it has in
-            // the free latent sets, in boxes of 128 bytes a row, under one fence and one wait (the
-            // rounds below have a fence each: 3.2 us for a partial against 1.7).
-            if (last_item && c_end > 0) {
-              c_end = 0;
-              const uint32_t stage_u32 = set_u32 + warp * 16384;
-              uint8_t* const stage = data + (stage_u32 - data_u32) + lane * 128;
-              const int sw = lane & 7;
-#pragma unroll
-              for (int c0 = 0; c0 < 128; c0 += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem + lane_base + kOCol + 128 * ch + c0, r);
-                tmem_wait_ld();
-                if (whole) {  // 32 columns: half a 128-byte row
-                  uint8_t* const box = stage + (c0 / 64) * 4096;
-#pragma unroll
-                  for (int u = 0; u < 4; ++u) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      const typename Pack<T>::T2 v =
-                          Pack<T>::make(u2f(r[8 * u + 2 * e]) * inv, u2f(r[8 * u + 2 * e + 1]) * inv);
-                      w[e] = *reinterpret_cast<const uint32_t*>(&v);
-                    }
-                    *reinterpret_cast<uint4*>(box + (((c0 / 8 % 8 + u) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                  }
-                } else {
-                  uint8_t* const box = stage + (c0 / 32) * 4096;
-#pragma unroll
-                  for (int u = 0; u < 8; ++u)
-                    *reinterpret_cast<float4*>(box + ((u ^ sw) << 4)) =
-                        make_float4(u2f(r[4 * u]) * inv, u2f(r[4 * u + 1]) * inv, u2f(r[4 * u + 2]) * inv,
-                                    u2f(r[4 * u + 3]) * inv);
-                }
-              }
-              fence_proxy_async_cta();
-              __syncwarp();
-              if (lane == 0) {
-                if (whole) {
-                  for (int k = 0; k < 2; ++k) tma_store_3d(&maps.o_lat, stage_u32 + 4096 * k, col0 + 64 * k, head0, ib);
-                } else {
-                  for (int k = 0; k < 4; ++k) tma_store_3d(part_map, stage_u32 + 4096 * k, col0 + 32 * k, head0, (int)slot);
-                }
-                bulk_commit_group();
-              }
-            }
-          }
 #pragma unroll 1
           for (int c0 = 0; c0 < c_end; c0 += 32) {
             uint32_t r[32];
@@ -1177,7 +1129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
           // the CTA exits
           if (lane == 0) {
             bulk_wait_read<0>();
-            mbar_arrive(bar(ctl->staged));
+            if constexpr (kShared) mbar_arrive(bar(ctl->staged));
           }
           __syncwarp();
           tc_fence_before();

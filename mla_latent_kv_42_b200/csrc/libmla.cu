@@ -642,13 +642,13 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
             host::encode_pages(&maps.page2, pool, bf16, (uint64_t)num_pages, tc::dec::kD * 2, 2) &&
             host::encode_pages(&maps.page4, pool, bf16, (uint64_t)num_pages, tc::dec::kD * 2, 4) &&
             host::encode_chunks(&maps.q9, q, bf16, (uint64_t)B * n_h, tc::dec::kD * 2, 9) &&
-            host::encode_heads_out(&maps.o_part, o_part, f32, 4, (uint64_t)n_h, (uint64_t)B + C, true) &&
+            host::encode_heads_out(&maps.o_part, o_part, f32, 4, (uint64_t)n_h, (uint64_t)B + C) &&
             host::encode_heads_out32(&maps.o_part_h, o_part, f32, 4, (uint64_t)n_h, (uint64_t)B + C);
   if (L.Mt > 0)
-    ok = ok && host::encode_heads_out(&maps.o_pre, o_pre, f32, 4, 128, (uint64_t)L.Mt + C, true) &&
+    ok = ok && host::encode_heads_out(&maps.o_pre, o_pre, f32, 4, 128, (uint64_t)L.Mt + C) &&
          host::encode_heads_out32(&maps.o_pre_h, o_pre, f32, 4, 128, (uint64_t)L.Mt + C);
   else
-    ok = ok && host::encode_heads_out(&maps.o_lat, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B, true) &&
+    ok = ok && host::encode_heads_out(&maps.o_lat, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B) &&
          host::encode_heads_out32(&maps.o_lat_h, o_lat, elem, 2, (uint64_t)n_h, (uint64_t)B);
   // a sequence's own item of at most 32 heads loads its own query rows, 8 at least, chunk by chunk
   const int own_q_rows = L.Mt > 0 && n_h <= 32 ? (n_h + 7) / 8 * 8 : 0;
