@@ -299,7 +299,8 @@ int mla_decode_attention_fp8(const mla_dims* dims, const void* q, const void* po
  * gain is given (MLA_ERR_INVALID_ARG otherwise). Any dims of mla_check_dims, one launch, no
  * workspace. A token whose slot is outside the table or the pool is not written and records
  * MLA_ERR_BAD_PAGE; slots of no token are left as they are. No two tokens of one call may have the
- * same slot (which of them it holds, or parts of which, is not defined). T == 0 is a no-op.
+ * same slot (which of them it holds, or parts of which, is not defined). 0 <= T <= 2^30
+ * (MLA_ERR_INVALID_ARG otherwise); T == 0 is a no-op.
  */
 int mla_norm_append_kv(const mla_dims* dims, const void* x, int64_t x_stride, const void* gain_c, const void* gain_r,
                        double eps, const int32_t* seq_idx, const int32_t* pos, const int32_t* block_table,
@@ -321,7 +322,8 @@ int mla_norm_append_kv_fp8(const mla_dims* dims, const void* x, int64_t x_stride
  * seq_idx[t]. The pairs may come in any order and more than once. With positions that fill whole
  * pages, `rows` is a run of pages: mla_read_kv_fp8 so turns a prefix of an FP8 cache into pages
  * that the element-type calls read. A token whose slot is outside the table or the pool gets a row
- * of zeros and records MLA_ERR_BAD_PAGE. `rows` must not overlap the pool. T == 0 is a no-op.
+ * of zeros and records MLA_ERR_BAD_PAGE. `rows` must not overlap the pool. 0 <= T <= 2^30
+ * (MLA_ERR_INVALID_ARG otherwise); T == 0 is a no-op.
  */
 int mla_read_kv(const mla_dims* dims, const void* pool, int32_t num_pages, const int32_t* seq_idx, const int32_t* pos,
                 const int32_t* block_table, int32_t num_seqs, int32_t max_pages, void* rows, int64_t rows_stride,

@@ -418,6 +418,13 @@ def _pool_shape(dims, pool, fp8):
     return (n, dims.page_size * (D + 8)) if fp8 else (n, dims.page_size, D)
 
 
+def _on(stream, t):
+    """A tensor of this call's own, kept from reuse until the stream it is used on is through with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _raw_stream(torch, here, stream):
     return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
 
@@ -474,7 +481,7 @@ def _read(fn, name, fp8, dims, pool, seq_idx, pos, block_table, out, stream):
                 (block_table, "block_table", i32, (S, width)),
                 *([] if out is None else [(out, "out", e, (T, D))]), strided="out")
     if out is None:
-        out = pool.new_empty((T, D), dtype=e)
+        out = _on(stream, pool.new_empty((T, D), dtype=e))
     code = fn(ctypes.byref(c_dims(dims)), pool.data_ptr(), shape[0], seq_idx.data_ptr(), pos.data_ptr(),
               block_table.data_ptr(), S, width, out.data_ptr(), out.stride(0) if T > 1 else D, T,
               _raw_stream(torch, here, stream))
@@ -503,6 +510,7 @@ def shared_prefix_attention(dims, q, pool, block_table, seq_lens, max_seq_len, s
     B = _sizes(q, 3, "q")[0]
     width = _sizes(block_table, 2, "block_table")[1]
     n_shared = _sizes(shared_pages, 1, "shared_pages")[0]
+    max_seq_len = int(max_seq_len)
     shape, q_shape = _pool_shape(dims, pool, False), (B, H, dims.d_c + dims.d_rope)
     if not (_ok(q, e, q_shape, here) and _ok(pool, e, shape, here) and _ok(block_table, i32, (B, width), here)
             and _ok(seq_lens, i32, (B,), here) and _ok(shared_pages, i32, (n_shared,), here)
@@ -515,13 +523,13 @@ def shared_prefix_attention(dims, q, pool, block_table, seq_lens, max_seq_len, s
                 *([] if lse is None else [(lse, "lse", torch.float32, (B, H))]),
                 *([] if ws is None else [(ws, "ws", ws.dtype, ws.shape)]))
     if o_lat is None:
-        o_lat = q.new_empty((B, H, dims.d_c))
+        o_lat = _on(stream, q.new_empty((B, H, dims.d_c)))
     if lse is None and want_lse:
-        lse = q.new_empty((B, H), dtype=torch.float32)
+        lse = _on(stream, q.new_empty((B, H), dtype=torch.float32))
     lib, cd = _lib(), ctypes.byref(c_dims(dims))
     if ws is None:
         n = lib.mla_workspace_size(cd, CALL_SHARED_PREFIX_ATTENTION, B, max_seq_len)
-        ws = q.new_empty(max(n, 16), dtype=torch.uint8)
+        ws = _on(stream, q.new_empty(max(n, 16), dtype=torch.uint8))
     code = lib.mla_shared_prefix_attention(
         cd, q.data_ptr(), pool.data_ptr(), shape[0], block_table.data_ptr(), width, seq_lens.data_ptr(), B,
         max_seq_len, shared_pages.data_ptr(), n_shared, o_lat.data_ptr(), None if lse is None else lse.data_ptr(),

@@ -453,6 +453,9 @@ rows::SlotMap slot_map(const mla_dims* d, const int32_t* bt, int32_t num_seqs, i
   return rows::SlotMap{bt, (int)num_seqs, (int)max_pages, (int)num_pages, (int)d->page_size};
 }
 
+// Tokens of one row call: their indices, and a grid's step past the last, stay in int32.
+constexpr int32_t kMaxRowTokens = 1 << 30;
+
 // CTAs for T tokens, a warp each, and `per_sm` CTAs to an SM at most.
 unsigned rows_grid(int T, int per_sm) {
   return (unsigned)std::min<long>(((long)T + rows::kWarps - 1) / rows::kWarps, (long)per_sm * device_sm_count());
@@ -492,7 +495,7 @@ int norm_append_call(const mla_dims* d, const void* x, int64_t x_stride, const v
                      int32_t max_pages, void* pool, int32_t num_pages, int32_t T, mla_stream_t stream) {
   const int r = check_dims_impl(d);
   if (r != MLA_OK) return r;
-  if (T < 0 || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxRowTokens || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return MLA_ERR_INVALID_ARG;
   if (x_stride < d->d_c + d->d_rope || x_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
   if ((g_c || g_r) && !(eps > 0.0 && std::isfinite(eps))) return MLA_ERR_INVALID_ARG;
   if (T == 0) {
@@ -514,7 +517,7 @@ int read_kv_call(const mla_dims* d, const void* pool, int32_t num_pages, const i
                  mla_stream_t stream) {
   const int r = check_dims_impl(d);
   if (r != MLA_OK) return r;
-  if (T < 0 || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxRowTokens || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return MLA_ERR_INVALID_ARG;
   if (out_stride < d->d_c + d->d_rope || out_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
   const int call = kFp8 ? MLA_CALL_READ_KV_FP8 : MLA_CALL_READ_KV;
   if (T == 0) {
@@ -539,12 +542,26 @@ bool shared_tc_eligible(const mla_dims* d) {
   return d->d_c == tc::dec::kDc && d->d_c + d->d_rope == tc::dec::kD && d->page_size == tc::dec::kPage;
 }
 
-// Whether the rows of B sequences are packed over the prefix.
-bool shared_packs(const mla_dims* d, int B) {
-  const long R = (long)B * d->n_heads;
-  if (shared_tc_eligible(d)) return (R + 127) / 128 < B;
-  return R > 16;
+inline long tiles_of(long tokens) { return (tokens + tc::dec::kTile - 1) / tc::dec::kTile; }
+
+// Whether the rows of B sequences are packed over a prefix of P tokens.
+// Tensor-core kernel: packing takes ceil(R / 128) items over the prefix in place of its tiles in every
+// sequence. In places of the kernel's list (a place is a tile's time, an item kItemUnits more) that
+// has to save more than the fp32 partials cost that every row then goes through, about a place per
+// 48 rows, and a few places for the further items. Measured on both sides, us packed / unpacked:
+// 16 heads, 4 sequences behind 512 tokens 20.3 / 18.3; 64 behind 128 21.0 / 22.7, 64 of 48 heads
+// behind 512 30.7 / 33.1; 128 of 80 heads behind 1024 84.7 / 83.3, 64 behind 4096 71.2 / 94.5;
+// 64 of 112 heads behind 4096 94.3 / 96.8. From 128 heads up a tile holds one sequence.
+// Narrow rows: packed from two sequences on (8 heads, 2 behind 512 tokens: 12.7 / 13.2; 4 behind
+// 4096: 16.2 / 28.5).
+bool shared_packs(const mla_dims* d, int B, long P) {
+  if (P == 0 || B < 2) return false;
+  if (!shared_tc_eligible(d)) return decode_mma_eligible(d);
+  const long R = (long)B * d->n_heads, Mt = (R + 127) / 128;
+  return B * tiles_of(P) - Mt * (tiles_of(P) + tc::kItemUnits) > 16 + R / 48;
 }
+// Whether some prefix makes the call pack (its workspace then has room for it).
+bool shared_may_pack(const mla_dims* d, int B) { return ((long)B * d->n_heads + 127) / 128 < B; }
 
 struct SharedTcLayout {
   int Mt;  // packed row tiles
@@ -602,7 +619,7 @@ SharedMmaPlan shared_mma_plan(const mla_dims* d, int B, int shared_len, int max_
 size_t ws_shared(const mla_dims* d, int B, int max_seq_len) {
   if (B <= 0 || max_seq_len < 1 || max_seq_len > kMaxSeqLen) return 0;
   const size_t plan = 2 * align256((size_t)B * 4);
-  if (shared_tc_eligible(d)) return shared_tc_layout(d, B, shared_packs(d, B)).bytes;
+  if (shared_tc_eligible(d)) return shared_tc_layout(d, B, shared_may_pack(d, B)).bytes;
   if (decode_mma_eligible(d)) {
     // every split count is at most these, whatever the prefix's length
     const long R = (long)B * d->n_heads, sm3 = 3L * device_sm_count();
@@ -781,7 +798,7 @@ int shared_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_
   plan.page_size = d->page_size;
   plan.shared_pages = shared_pages;
   const bool tc_path = shared_tc_eligible(d), mma_path = decode_mma_eligible(d);
-  plan.n_shared = (tc_path || mma_path) && shared_packs(d, B) ? num_shared : 0;
+  plan.n_shared = shared_packs(d, B, (long)num_shared * d->page_size) ? num_shared : 0;
   plan.lanes = 1;  // as many threads to a sequence as the block has for B of them
   while (plan.lanes < 32 && 2 * plan.lanes * B <= 1024) plan.lanes *= 2;
   int32_t n = 0;

@@ -101,6 +101,9 @@ EDGES = [1, 0, 64, 63, 65, 128, 129, 300, 2]
     (5, 27, 9, "bf16"), (33, 5, 2, "fp16"), (64, 2, 5, "bf16"), (64, 23, 4, "fp16"), (65, 11, 3, "bf16"),
     (96, 9, 2, "bf16"), (127, 130, 1, "bf16"), (128, 9, 3, "bf16"), (128, 1, 4, "fp16"), (16, 1, 4, "bf16"),
     (32, 40, 65, "bf16"), (16, 5, 0, "bf16"), (128, 4, 0, "bf16"),
+    # packed rows whose last tile is short, sequences that straddle tiles, fewer places than SM pairs
+    (33, 40, 9, "bf16"), (64, 40, 17, "fp16"), (65, 60, 33, "bf16"), (96, 64, 33, "bf16"), (100, 64, 41, "fp16"),
+    (48, 30, 9, "fp16"), (16, 9, 40, "fp16"), (1, 7, 40, "bf16"), (3, 50, 201, "bf16"), (17, 33, 7, "bf16"),
 ])
 def test_wide_rows(heads, B, shared, dtype):
     d = P.with_(n_heads=heads, dtype=dtype)
@@ -179,20 +182,21 @@ def test_agrees_with_decode_and_repeats_bitwise(d):
     assert float((lse - ref_l).abs().max()) <= 2.0 ** -8
 
 
-@pytest.mark.parametrize("d", [P.with_(n_heads=16), P.with_(n_heads=96), P, R, GENERIC],
-                         ids=["h16", "h96", "h128", "narrow", "generic"])
-def test_rejected_sequences(d):
+@pytest.mark.parametrize("d,shared", [(P.with_(n_heads=16), 2), (P.with_(n_heads=16), 40), (P.with_(n_heads=96), 2),
+                                      (P.with_(n_heads=80), 60), (P, 2), (R, 2), (GENERIC, 2)],
+                         ids=["h16", "h16-packed", "h96", "h80-packed", "h128", "narrow", "generic"])
+def test_rejected_sequences(d, shared):
     """A bad length or own page rejects its sequence alone; a bad shared page every one that has it."""
-    lens = batch(12, 2 * d.page_size, [1, 70, 130])
+    lens = batch(12, shared * d.page_size, [1, 70, 130])
     lens[5] = 3  # idle
-    c = Case(d, lens, 2, seed=7)
+    c = Case(d, lens, shared, seed=7)
     good_o, good_l = c.run()
     assert M.read_device_status() == 0
     lens_bad = c.lens.clone()
     lens_bad[2], lens_bad[8] = 0, c.longest + 1
     table_bad = c.table.clone()
-    table_bad[4, 2] = len(c.pool)
-    table_bad[7, 2] = -1
+    table_bad[4, shared] = len(c.pool)
+    table_bad[7, shared] = -1
     o, lse = M.shared_prefix_attention(d, c.q, c.pool, table_bad, lens_bad, c.longest, c.shared)
     assert M.read_device_status() in (-7, -8)
     for b in range(12):
@@ -211,9 +215,10 @@ def test_rejected_sequences(d):
     assert M.read_device_status() == 0 and torch.equal(o, good_o) and torch.equal(lse, good_l)
 
 
-def test_without_lse_given_outputs_and_no_sequences():
+@pytest.mark.parametrize("shared", [2, 30])
+def test_without_lse_given_outputs_and_no_sequences(shared):
     d = P.with_(n_heads=16)
-    c = Case(d, batch(5, 128, [1, 9]), 2, seed=1)
+    c = Case(d, batch(5, 64 * shared, [1, 9]), shared, seed=1)
     o, lse = c.run()
     out = torch.empty_like(o)
     ws = torch.empty(M.workspace_size(d, M.CALL_SHARED_PREFIX_ATTENTION, 5, c.longest), dtype=torch.uint8,
@@ -221,7 +226,7 @@ def test_without_lse_given_outputs_and_no_sequences():
     ws.fill_(0xFF)  # NaN partials: nothing is read that this call did not write
     got, none = c.run(o_lat=out, want_lse=False, ws=ws)
     assert got is out and none is None and torch.equal(got, o)
-    e, l = M.shared_prefix_attention(d, c.q[:0], c.pool, c.table[:0], c.lens[:0], 200, c.shared)
+    e, l = M.shared_prefix_attention(d, c.q[:0], c.pool, c.table[:0], c.lens[:0], c.longest, c.shared)
     assert e.shape == (0, 16, 512) and l.shape == (0, 16)
     assert M.last_launch_count(M.CALL_SHARED_PREFIX_ATTENTION) == 0
     assert M.read_device_status() == 0
@@ -229,8 +234,8 @@ def test_without_lse_given_outputs_and_no_sequences():
 
 @pytest.mark.parametrize("d", [P.with_(n_heads=16), R], ids=["h16", "narrow"])
 def test_captured_and_replayed_as_lengths_grow(d):
-    lens = batch(8, 3 * d.page_size, [1, 60, 126])
-    c = Case(d, lens + 4, 3, seed=2)  # rows for every step below
+    lens = batch(8, 24 * d.page_size, [1, 60, 126])
+    c = Case(d, lens + 4, 24, seed=2)  # rows for every step below
     c.lens.copy_(torch.from_numpy(lens.astype(np.int32)))
     ws = torch.empty(M.workspace_size(d, M.CALL_SHARED_PREFIX_ATTENTION, 8, c.longest), dtype=torch.uint8,
                      device="cuda")
@@ -269,14 +274,14 @@ def test_together_fp8_prefix_written_read_back_and_shared():
     back into element-type pages, the sequences' own rows written beside them, and one attention
     over both."""
     d = P.with_(n_heads=16)
-    page, shared, B = d.page_size, 5, 9
+    page, shared, B = d.page_size, 12, 9
     g = torch.Generator(device="cuda").manual_seed(0)
     i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
     gain = (1 + 0.1 * torch.randn(d.d_c, device="cuda", generator=g)).bfloat16()
     n = shared * page
     x = torch.randn((n, d.D), device="cuda", generator=g).bfloat16()
     cold = torch.empty((shared, M.fp8_page_bytes(d)), dtype=torch.uint8, device="cuda")
-    pos, zero, cold_table = i32(list(range(n))), i32([0] * n), i32([[4, 2, 0, 1, 3]])
+    pos, zero, cold_table = i32(list(range(n))), i32([0] * n), i32([[4, 2, 0, 11, 3, 7, 5, 10, 1, 6, 9, 8]])
     M.norm_append_kv_fp8(d, x, zero, pos, cold_table, cold, gain_c=gain)
     lens = batch(B, n, [1, 64, 70])
     c = Case(d, lens, shared, seed=11)

@@ -36,7 +36,7 @@ def test_norm_append_refusals(lib, name, d):
     assert f(*swap(args, _2=d.D - 8)) == -1 and f(*swap(args, _2=d.D + 4)) == -1
     for eps in (0.0, -1.0, float("inf"), float("nan")):
         assert f(*swap(args, _5=eps)) == -1
-    for at, v in ((9, 0), (10, 0), (12, 0), (13, -1)):
+    for at, v in ((9, 0), (10, 0), (12, 0), (13, -1), (13, (1 << 30) + 1)):
         assert f(*swap(args, **{f"_{at}": v})) == -1
     assert f(*swap(args, _13=0)) == 0 and f(*swap(args, _13=0, _1=None)) == 0
     bad = M.c_dims(d)
@@ -54,7 +54,7 @@ def test_read_refusals(lib, name):
     for at in (1, 8):
         assert f(*swap(args, **{f"_{at}": MISALIGNED})) == -4
     assert f(*swap(args, _9=d.D - 8)) == -1 and f(*swap(args, _9=d.D + 1)) == -1
-    for at, v in ((2, 0), (6, 0), (7, 0), (10, -1)):
+    for at, v in ((2, 0), (6, 0), (7, 0), (10, -1), (10, (1 << 30) + 1)):
         assert f(*swap(args, **{f"_{at}": v})) == -1
     assert f(*swap(args, _10=0)) == 0
 
