@@ -20,23 +20,25 @@ constexpr int kLatGroups = 2; // 8-element groups of the latent part per lane: d
 constexpr int kMaxR = 9;      // pairs of the rotated part per lane: d_rope / 2 <= 284 <= 32 kMaxR
 constexpr int kPowers = 9;    // 32 kMaxR < 2^9
 constexpr int kWarps = 8;     // per CTA
-// CTAs per SM at most; warps then loop over tokens. A writer keeps its registers (gains, frequencies)
-// and requests a token ahead: four CTAs fit, more only repeat its start (8192 tokens: 7.3 us with
-// three or four, 8.2 with eight). A reader has nothing to keep (131072 tokens: 44.5 us; with two
-// or four tokens to a warp at a time 43.8 to 46, but 1021 tokens 2.6 and 3.2 us against 2.2).
-constexpr int kAppendPerSm = 4, kReadPerSm = 32;
+// CTAs per SM at most; warps then loop over tokens. A writer keeps what is the same for every token
+// in registers and requests a token ahead: as many CTAs as fit (8192 tokens to e4m3: 6.9 us with
+// three, 7.5 with four, 10.2 with five at 48 registers a thread, 7.5 with eight of which three fit).
+// A reader has nothing to keep (131072 tokens: 41.9 us).
+constexpr int kAppendPerSm = 3, kReadPerSm = 32;
 
-// Slot (row of the pool) of position p of sequence s, or -1 if it is outside the table or the pool.
+// Page and row in it of position p of sequence s; page -1 if it is outside the table or the pool.
+struct Slot {
+  int page, row;
+};
 struct SlotMap {
   const int* bt;  // [num_seqs, max_pages]
   int num_seqs, max_pages, num_pages, page_size;
-  __device__ __forceinline__ long operator()(int s, int p) const {
-    if (s < 0 || s >= num_seqs || p < 0) return -1;
+  __device__ __forceinline__ Slot operator()(int s, int p) const {
+    if (s < 0 || s >= num_seqs || p < 0) return {-1, 0};
     const int lp = p / page_size;
-    if (lp >= max_pages) return -1;
+    if (lp >= max_pages) return {-1, 0};
     const int page = bt[(long)s * max_pages + lp];
-    if (page < 0 || page >= num_pages) return -1;
-    return (long)page * page_size + (p - lp * page_size);
+    return {page < num_pages ? page : -1, p - lp * page_size};  // (a negative entry stays negative)
   }
 };
 
@@ -94,7 +96,7 @@ struct AppendArgs {
 // What a lane needs of the gains and the frequencies (doubles) is the same for every token and
 // stays in its registers.
 template <typename T, bool kFp8, int kR>
-__global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::AppendArgs a) {
+__global__ void __launch_bounds__(32 * rows::kWarps, kR == 1 ? rows::kAppendPerSm : 1) k_norm_append(const rows::AppendArgs a) {
   using namespace rows;
   using P2 = typename Pack<T>::T2;
   constexpr int kC = kLatGroups;
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
   request(t);
   for (; t < a.T; t += n_warps) {
     const int pos = p;
-    const long slot = a.slot(seq, pos);  // used at the end: the table's read overlaps the arithmetic
+    const Slot at = a.slot(seq, pos);  // used at the end: the table's read overlaps the arithmetic
     float v[kC][8];
     float2 r[kR];
 #pragma unroll
@@ -190,12 +192,12 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
       mc = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mc)));
       mr = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mr)));
     }
-    if (slot < 0) {
+    if (at.page < 0) {
       if (lane == 0) record_error(MLA_ERR_BAD_PAGE);
       continue;
     }
     if constexpr (!kFp8) {
-      T* dst = static_cast<T*>(a.pool) + slot * a.D;
+      T* dst = static_cast<T*>(a.pool) + ((long)at.page * a.slot.page_size + at.row) * a.D;
 #pragma unroll
       for (int i = 0; i < kC; ++i)
         if (lane + 32 * i < Gc) {
@@ -218,10 +220,8 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
       // scales whose reciprocal or whose products with values are not normal divide as they are
       const bool plain = !(fminf(sc, sr) > 0x1p-100f && fmaxf(sc, sr) < 0x1p100f);
       const int ps = a.slot.page_size;
-      const long page = slot / ps;
-      const int row = (int)(slot - page * ps);
-      uint8_t* const pg = static_cast<uint8_t*>(a.pool) + page * fp8::page_bytes(ps, a.D);
-      uint8_t* const dst = pg + (long)row * a.D;
+      uint8_t* const pg = static_cast<uint8_t*>(a.pool) + at.page * fp8::page_bytes(ps, a.D);
+      uint8_t* const dst = pg + (long)at.row * a.D;
       auto store = [&](auto divide) {
         auto e4m3x2 = [&](float x, float y, float s, float inv) {
           return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(divide(x, s, inv), divide(y, s, inv)), __NV_SATFINITE,
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_norm_append(const rows::A
       };
       if (plain) store([](float x, float s, float) { return x / s; });
       else store([](float x, float s, float inv) { return quotient(x, s, inv); });
-      if (lane == 0) *reinterpret_cast<float2*>(pg + (long)ps * a.D + 8 * row) = make_float2(sc, sr);
+      if (lane == 0) *reinterpret_cast<float2*>(pg + (long)ps * a.D + 8L * at.row) = make_float2(sc, sr);
     }
   }
 }
@@ -259,9 +259,10 @@ struct ReadArgs {
 };
 }  // namespace rows
 
-// A warp per token. Bound by the writes: 151 MB of rows out of 76 MB of e4m3 pages take 44.5 us, and
-// setting 151 MB to zero takes 41.5 (3.6 TB/s; reads run beside it). A token without a valid slot
-// becomes a zero row and records MLA_ERR_BAD_PAGE.
+// A warp per token. Bound by the writes: 151 MB of rows out of 76 MB of e4m3 pages take 41.9 us, and
+// setting 151 MB to zero takes 41.5 (3.6 TB/s; the reads run beside it). Two, four or eight tokens to
+// a warp at a time, or stores that do not stay in L2, were no faster; 1021 tokens then took 2.6, 3.2
+// and 4.6 us against 2.0. A token without a valid slot becomes a zero row and records MLA_ERR_BAD_PAGE.
 template <typename T, bool kFp8>
 __global__ void __launch_bounds__(32 * rows::kWarps) k_read_rows(const rows::ReadArgs a) {
   using namespace rows;
@@ -274,24 +275,23 @@ __global__ void __launch_bounds__(32 * rows::kWarps) k_read_rows(const rows::Rea
   if (threadIdx.x == 0) griddep_launch();
   const int n_warps = gridDim.x * kWarps;
   for (int t = blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += n_warps) {
-    const long slot = a.slot(a.seq_idx[t], a.pos[t]);
-    if (slot < 0 && lane == 0) record_error(MLA_ERR_BAD_PAGE);
+    const Slot at = a.slot(a.seq_idx[t], a.pos[t]);
+    const bool there = at.page >= 0;
+    if (!there && lane == 0) record_error(MLA_ERR_BAD_PAGE);
     Raw raw[kGroups];
     float2 sc = make_float2(0.f, 0.f);
     const uint8_t* src;
     if constexpr (kFp8) {
-      const long page = slot / ps;
-      const int row = (int)(slot - page * ps);
-      const uint8_t* pg = static_cast<const uint8_t*>(a.pool) + page * fp8::page_bytes(ps, a.D);
-      src = pg + (long)row * a.D;
-      if (slot >= 0) sc = *reinterpret_cast<const float2*>(pg + (long)ps * a.D + 8 * row);
+      const uint8_t* pg = static_cast<const uint8_t*>(a.pool) + at.page * fp8::page_bytes(ps, a.D);
+      src = pg + (long)at.row * a.D;
+      if (there) sc = *reinterpret_cast<const float2*>(pg + (long)ps * a.D + 8L * at.row);
     } else {
-      src = static_cast<const uint8_t*>(a.pool) + slot * a.D * (long)sizeof(T);
+      src = static_cast<const uint8_t*>(a.pool) + ((long)at.page * ps + at.row) * a.D * (long)sizeof(T);
     }
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       const int g = lane + 32 * i;
-      raw[i] = slot >= 0 && g < G ? *reinterpret_cast<const Raw*>(src + sizeof(Raw) * g) : Raw{};
+      raw[i] = there && g < G ? *reinterpret_cast<const Raw*>(src + sizeof(Raw) * g) : Raw{};
     }
     T* dst = static_cast<T*>(a.out) + (long)t * a.out_stride;
 #pragma unroll
