@@ -316,15 +316,20 @@ __device__ void attn_mma_item(const MmaAttnArgs& a, int b, int split, uint8_t* s
         acc = fmaf(f, wo[(w * 16 + row) * d_c + col], acc);
       }
     }
-    const float inv = l > 0.f ? 1.f / (l + dif) : 0.f;
+    if constexpr (kOwn) {
+      if (m == -INFINITY)  // no tokens, or scores of NaN alone: 0, or the NaN goes through
+        for (int w = 0; w < kWarps; ++w) l += w_ml[w][row][1];
+    }
+    const bool some = kOwn ? l != 0.f : l > 0.f;
+    const float inv = some ? 1.f / (l + dif) : 0.f;
     const long bh = (long)b * n_h + row;
     if (n_splits == 1) {
       Out<T>::put(o_lat + bh * d_c + col, acc * inv);
-      if (col == 0 && lse_out != nullptr) lse_out[bh] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (col == 0 && lse_out != nullptr) lse_out[bh] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     } else {
       const long part = bh * n_splits + split + (kOwn ? a.part0 : 0);
       o_part[part * d_c + col] = acc * inv;
-      if (col == 0) lse_part[part] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (col == 0) lse_part[part] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
 }

@@ -113,13 +113,13 @@ __global__ void __launch_bounds__(256) k_lse_merge_warp(const float* __restrict_
   for (int s = lane + 32; s < n_splits; s += 32) mx = fmaxf(mx, lp[s]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  auto weight = [&](float l) { return l > -INFINITY ? exp2f((l - mx) * kLog2e) : 0.f; };  // -inf: no tokens
+  auto weight = [&](float l) { return l == -INFINITY ? 0.f : exp2f((l - mx) * kLog2e); };  // -inf: no tokens
   const float w_lane = weight(l_lane);
   float z = w_lane;
   for (int s = lane + 32; s < n_splits; s += 32) z += weight(lp[s]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const float inv = z != 0.f ? 1.f / z : 0.f;
   const float* src0 = o_part + bh * n_splits * d_c;
   for (int c0 = 0; c0 < d_c; c0 += 128) {
     const int c = c0 + 4 * lane;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256) k_lse_merge_warp(const float* __restrict_
     Out<T>::put(out + 2, acc.z * inv);
     Out<T>::put(out + 3, acc.w * inv);
   }
-  if (lse_out != nullptr && lane == 0) lse_out[bh] = z > 0.f ? mx + logf(z) : -INFINITY;
+  if (lse_out != nullptr && lane == 0) lse_out[bh] = z != 0.f ? mx + logf(z) : -INFINITY;
 }
 
 }  // namespace mla

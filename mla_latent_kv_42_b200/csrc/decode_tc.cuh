@@ -185,8 +185,8 @@ __device__ __forceinline__ ItemIter item_iter_at(const int4& at, int cluster, in
   const long T = at.w;
   return ItemIter{T * cluster / nclusters, T * (cluster + 1) / nclusters, at.x, at.y, at.z};
 }
-// kUnits: places an item takes in the list before its tiles, for its share of the split (kItemUnits
-// below); 0 where the list holds tiles alone.
+// kUnits: places an item takes in the list before its tiles, for its share of the split (kItemUnits);
+// 0 where the list holds tiles alone.
 template <int kUnits>
 __device__ __forceinline__ bool next_item(ItemIter& it, const int* prefix, Item& out) {
   if constexpr (kUnits == 0) {
@@ -416,7 +416,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
     if constexpr (kShared) return b < p.prefix_items ? 128 * b : (b - p.prefix_items) * p.n_h;
     else return b * p.n_h;
   };
-
   auto small_q = [&](int b) {
     if constexpr (kShared) return b >= p.prefix_items && p.own_q_rows > 0;
     else return false;
@@ -992,8 +991,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
                     fmaf(four[2], __bfloat162float(ctl->xh[0][l0 + 64]),
                          fmaf(four[3], __bfloat162float(ctl->xh[1][l0 + 64]), l))));
           }
-          const float inv = denom > 0.f ? 1.f / denom : 0.f;
-          const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+          // (kShared: a NaN among the scores, which only its own row sees, goes through to the output)
+          const bool some = kShared ? l != 0.f : l > 0.f;
+          const float inv = some ? 1.f / denom : 0.f;
+          const float lse = some ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
           const Item& it = c.item;
           bool whole = it.t0 == 0 && it.t1 == it.n_b, packed = false;
           int ib = it.b, n_rows = p.n_h;  // the item among its kind, its query rows

@@ -267,7 +267,7 @@ __device__ __forceinline__ void merge_row(const shared::MergeArgs& a, const shar
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_red[w]);
   }
-  auto weight_of = [&](float l) { return l > -INFINITY ? exp2f((l - mx) * kLog2e) : 0.f; };
+  auto weight_of = [&](float l) { return l == -INFINITY ? 0.f : exp2f((l - mx) * kLog2e); };  // a NaN stays
   const float w_lane = weight_of(mine);
   float z = 0.f;
   if (!many) {
@@ -316,7 +316,7 @@ __device__ __forceinline__ void merge_row(const shared::MergeArgs& a, const shar
       acc[0].w += o.w;
     }
   }
-  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const float inv = z != 0.f ? 1.f / z : 0.f;
   T* const out = static_cast<T*>(a.o_lat) + (long)r * tc::dec::kDc + col;
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
@@ -324,7 +324,7 @@ __device__ __forceinline__ void merge_row(const shared::MergeArgs& a, const shar
                                          Pack<T>::make(acc[j].z * inv, acc[j].w * inv)};
     *reinterpret_cast<uint2*>(out + 4 * kLanes * j) = *reinterpret_cast<const uint2*>(two);
   }
-  if (a.lse_out != nullptr && tid == 0) a.lse_out[r] = z > 0.f ? mx + logf(z) : -INFINITY;
+  if (a.lse_out != nullptr && tid == 0) a.lse_out[r] = z != 0.f ? mx + logf(z) : -INFINITY;
 }
 
 template <typename T, int kLanes, int kGroups>
@@ -524,7 +524,7 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
       rounded += __shfl_xor_sync(0xffffffffu, rounded, o);
     }
     if (rows[h2] >= R) continue;
-    const bool some = live[h2] && l > 0.f;
+    const bool some = live[h2] && l != 0.f;  // a NaN goes through
     const float inv = some ? 1.f / rounded : 0.f;
     const long part = (long)rows[h2] * g0.n_splits + split;
 #pragma unroll

@@ -252,6 +252,25 @@ def test_captured_and_replayed_as_lengths_grow(d):
     assert M.read_device_status() == 0
 
 
+@pytest.mark.parametrize("d,shared", [(P.with_(n_heads=16), 30), (P.with_(n_heads=16), 2), (P, 3), (R, 5), (R, 0)],
+                         ids=["h16-packed", "h16", "h128", "narrow", "narrow-alone"])
+def test_not_a_number_stays_in_its_sequence(d, shared):
+    """A NaN in a sequence's queries, or in one of its own cached rows, is in that sequence's output
+    (its head's, or all heads') and changes no other bit."""
+    c = Case(d, batch(12, shared * d.page_size, [70, 1, 200]).clip(1), shared, seed=12)
+    o, lse = c.run()
+    c.q[3, 1, 5] = float("nan")
+    c.pool[c.table[6, (int(c.lens_np[6]) - 1) // d.page_size].long(), (int(c.lens_np[6]) - 1) % d.page_size] = float("nan")
+    got_o, got_l = c.run()
+    assert M.read_device_status() == 0
+    same = [b for b in range(12) if b not in (3, 6)]
+    assert torch.equal(got_o[same], o[same]) and torch.equal(got_l[same], lse[same])
+    heads = [h for h in range(d.n_heads) if h != 1]
+    assert torch.equal(got_o[3, heads], o[3, heads]) and torch.equal(got_l[3, heads], lse[3, heads])
+    assert bool(got_o[3, 1].isnan().all()) and bool(got_l[3, 1].isnan())
+    assert bool(got_o[6].isnan().all()) and bool(got_l[6].isnan().all())
+
+
 def test_two_streams_at_once():
     cases = [Case(P.with_(n_heads=16), batch(20, 64 * 30, EDGES), 30, seed=s) for s in (1, 2)]
     want = [c.run() for c in cases]
