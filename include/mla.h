@@ -375,7 +375,7 @@ int32_t mla_last_launch_count(int32_t call);
 typedef struct CUevent_st* mla_event_t;
 
 /* Profiling hook (not part of the method): from this call on, every mla_decode_attention (and
- * _noalloc) call made by this host thread records `before` on its stream immediately before the
+ * _noalloc) and mla_shared_prefix_attention call made by this host thread records `before` on its stream immediately before the
  * attention kernel and `after` immediately after it (mla_prefill_attention records them around the
  * attention kernel of each of its launch groups, so afterwards they bracket the last group's), so that the kernel's own duration can be
  * read with cudaEventElapsedTime apart from the planner and the split-KV merge launched in the

@@ -570,19 +570,24 @@ class LayerState:
     block_table: object  # int32 [B, max_pages]
 
 
-def layer_step(st: LayerState, h, pos, seq_idx, seq_lens, max_seq_len, ws=None, out=None, stream=None):
+def layer_step(st: LayerState, h, pos, seq_idx, seq_lens, max_seq_len, ws=None, out=None, stream=None,
+               shared_pages=None):
     """One decode step of one layer through the four C-ABI calls; returns (u, q, o_lat, lse).
 
     ``pos`` = cached length of each sequence (the new token's position), ``seq_lens`` = pos + 1.
     ``ws`` is one byte buffer at least as large as the largest of the four workspaces (the calls
-    run in order on one stream, so they can share it).
+    run in order on one stream, so they can share it). ``shared_pages``: the pages that the sequences
+    begin with in common; the attention is then shared_prefix_attention's.
     """
     d, w = st.dims, st.w
     out = out or {}
     append_kv(d, h, w["w_dkv_kr"], seq_idx, pos, st.block_table, st.pool, ws=ws, stream=stream)
     q = absorb_query(d, h, w["w_dq"], w["w_uq_qr"], w["w_uk"], pos, q_out=out.get("q"), ws=ws, stream=stream)
-    o_lat, lse = decode_attention(d, q, st.pool, st.block_table, seq_lens, max_seq_len, o_lat=out.get("o_lat"),
-                                  lse=out.get("lse"), want_lse=out.get("want_lse", True), ws=ws, stream=stream)
+    outs = dict(o_lat=out.get("o_lat"), lse=out.get("lse"), want_lse=out.get("want_lse", True), ws=ws, stream=stream)
+    if shared_pages is None:
+        o_lat, lse = decode_attention(d, q, st.pool, st.block_table, seq_lens, max_seq_len, **outs)
+    else:
+        o_lat, lse = shared_prefix_attention(d, q, st.pool, st.block_table, seq_lens, max_seq_len, shared_pages, **outs)
     u = out_proj(d, o_lat, w["w_uv"], w["w_o"], u=out.get("u"), ws=ws, stream=stream)
     return u, q, o_lat, lse
 
@@ -625,5 +630,7 @@ def layer_step_small(st: LayerState, h, seq_lens, max_seq_len, ws=None, out=None
     return u, q, o_lat, lse
 
 
-def step_workspace_bytes(dims, B: int, max_seq_len: int) -> int:
-    return max(workspace_size(dims, c, B, max_seq_len) for c in range(4))
+def step_workspace_bytes(dims, B: int, max_seq_len: int, shared: bool = False) -> int:
+    """Bytes that every call of a ``layer_step`` fits in (``shared``: one with shared pages)."""
+    calls = [CALL_APPEND_KV, CALL_ABSORB_QUERY, CALL_DECODE_ATTENTION, CALL_OUT_PROJ]
+    return max(workspace_size(dims, c, B, max_seq_len) for c in calls + [CALL_SHARED_PREFIX_ATTENTION] * shared)

@@ -693,9 +693,11 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   p.prefix_len = plan.n_shared * plan.page_size;
   p.own_q_rows = own_q_rows;
   p.lse_pre = reinterpret_cast<float*>(ws + L.lse_pre);
+  mark_before(st);
   if (launch_pdl(tc::k_decode_tc<T, false, true>, dim3(2 * C), dim3(tc::dec::kThreads), tc::dec::kSmem, st, maps, p) !=
       cudaSuccess)
     return MLA_ERR_CUDA;
+  mark_after(st);
   const shared::MergeArgs m{o_pre, p.lse_pre, o_part, p.lse_part, plan.tile_prefix, plan.pairs, plan.first, B, n_h,
                             L.Mt, C, o_lat, lse_out};
   const unsigned R = (unsigned)((long)B * n_h);
@@ -763,6 +765,7 @@ int shared_mma_impl(const mla_dims* d, const void* q, const void* pool, int32_t 
   a.own_splits = s.own_splits;
   const long blocks = (long)s.row_tiles * s.pre_splits + (long)B * s.own_splits;
   bool ok = false;
+  mark_before(st);
   switch ((D + 31) / 32) {  // D <= 192
     case 1: ok = launch_shared_mma<T, 2>(a, (unsigned)blocks, st); break;
     case 2: ok = launch_shared_mma<T, 4>(a, (unsigned)blocks, st); break;
@@ -772,6 +775,7 @@ int shared_mma_impl(const mla_dims* d, const void* q, const void* pool, int32_t 
     default: ok = launch_shared_mma<T, 12>(a, (unsigned)blocks, st); break;
   }
   if (!ok) return MLA_ERR_CUDA;
+  mark_after(st);
   launches += 2;
   if (parts > 1) {
     if (launch_pdl(k_lse_merge_warp<T>, dim3((unsigned)((R + 7) / 8)), dim3(256), 0, st,

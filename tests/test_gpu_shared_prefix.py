@@ -288,6 +288,30 @@ def test_two_streams_at_once():
     assert M.read_device_status() == 0
 
 
+@pytest.mark.parametrize("d", [R, P.with_(n_heads=16, d_model=1024, d_cq=256)], ids=["running", "h16"])
+def test_layer_step_behind_a_shared_prefix(d):
+    """A whole layer step with shared pages: the step without them to the rounding of o_lat (half a step
+    on either side, then a product over n_h d_h values of it), its appended rows bit for bit."""
+    from mla_latent_kv_42_b200 import LayerState
+    lens = batch(24, 20 * d.page_size, [1, 70, 64])
+    c = Case(d, lens, 20, seed=14)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    e = synth.storage_dtype(d)
+    w = {k: (0.02 * torch.randn(s, device="cuda", generator=g)).to(e) for k, s in synth._weight_shapes(d).items()}
+    h = torch.randn((24, d.d_model), device="cuda", generator=g).to(e)
+    seq = torch.arange(24, dtype=torch.int32, device="cuda")
+    other = c.pool.clone()
+    ws = torch.empty(M.step_workspace_bytes(d, 24, c.longest, shared=True), dtype=torch.uint8, device="cuda")
+    u, q, o, lse = M.layer_step(LayerState(d, w, c.pool, c.table), h, c.lens - 1, seq, c.lens, c.longest, ws=ws,
+                                shared_pages=c.shared)
+    u2, q2, o2, lse2 = M.layer_step(LayerState(d, w, other, c.table), h, c.lens - 1, seq, c.lens, c.longest)
+    assert M.read_device_status() == 0
+    assert torch.equal(c.pool.view(torch.int16), other.view(torch.int16)) and torch.equal(q, q2)
+    assert float((o.float() - o2.float()).abs().max()) <= 2.0 ** -6 * float(o2.float().abs().max())
+    assert float((u.float() - u2.float()).abs().max()) <= 2.0 ** -5 * float(u2.float().abs().max())
+    assert float((lse - lse2).abs().max()) <= 2.0 ** -8
+
+
 def test_together_fp8_prefix_written_read_back_and_shared():
     """The calls as they are used: a prefix normalised, rotated and quantised into the FP8 cache, read
     back into element-type pages, the sequences' own rows written beside them, and one attention
