@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "fp8.cuh"
+#include "shared_plan.cuh"
 #include "tc_common.cuh"
 
 namespace mla {
@@ -142,11 +143,6 @@ struct SharedTcMaps : DecodeTcMaps {
   CUtensorMap o_pre, o_pre_h;  // partials of the prefix items: (512 columns, 128 rows, items + C)
   CUtensorMap q1;              // queries with boxes of one chunk x own_q_rows rows (own_q_rows > 0)
 };
-// A pair spends on an item, beside its tiles, the time of about kItemUnits more: its queries'
-// load, the pipeline's fill and the epilogue (a one-tile item took 6.7 us where a tile of a long
-// one takes 2.6). With items counted by tiles alone, 256 one-token sequences behind 32768 shared
-// tokens fell to the last pairs and the call took 1520 us.
-constexpr int kItemUnits = 2;
 struct SharedTcParams : DecodeTcParams {
   const int* first;         // [B], -1 for a rejected sequence (which has no tiles)
   const int* shared_pages;  // pages of the prefix
@@ -154,6 +150,8 @@ struct SharedTcParams : DecodeTcParams {
   int prefix_items, prefix_len;
   int own_q_rows;           // n_h rounded up to 8 where a sequence's rows fit one small box, else 0
   float* lse_pre;           // [items + C][128]
+  int fold;                 // every CTA makes the plan (all write the same values), no kernel before does
+  shared::PlanArgs plan;
 };
 
 // Tiles [t0, t1) of sequence b handled by this pair (n_b = tiles of the sequence).
@@ -185,8 +183,8 @@ __device__ __forceinline__ ItemIter item_iter_at(const int4& at, int cluster, in
   const long T = at.w;
   return ItemIter{T * cluster / nclusters, T * (cluster + 1) / nclusters, at.x, at.y, at.z};
 }
-// kUnits: places an item takes in the list before its tiles, for its share of the split (kItemUnits);
-// 0 where the list holds tiles alone.
+// kUnits: places an item takes in the list before its tiles, for its share of the split (kItemUnits
+// of shared_plan.cuh); 0 where the list holds tiles alone.
 template <int kUnits>
 __device__ __forceinline__ bool next_item(ItemIter& it, const int* prefix, Item& out) {
   if constexpr (kUnits == 0) {
@@ -249,6 +247,7 @@ struct CursorOf {
 
 // Most SM pairs one call spreads its tiles over (the merge kernel lists a sequence's pairs).
 constexpr int kMaxDecodeClusters = 128;
+static_assert(kMaxDecodeClusters <= shared::kMaxPairs, "pairs of the plan");
 // A sequence whose tiles fall to pairs c0 < c1 is merged by the merge kernel from the pairs'
 // partials (fp32 o / l and lse in slot b + c). The planner gives each sequence
 // c0 | c1 << 16 | all << 28 (all: every pair has tiles, so the slots are b + c0 .. b + c1),
@@ -309,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
                 const std::conditional_t<kShared, SharedTcParams, DecodeTcParams> p) {
   using namespace dec;
   static_assert(!(F8 && kShared), "the shared prefix is read from the element-type cache");
-  using Cursor = CursorOf<kShared ? kItemUnits : 0>;
+  using Cursor = CursorOf<kShared ? shared::kItemUnits : 0>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl* ctl = reinterpret_cast<Ctrl*>(data + kDataBytes);
@@ -372,6 +371,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F8 ? dec::kThreadsF8
   if (threadIdx.x == 0) griddep_launch();
   griddep_wait();  // the plan, the query and the cache come from earlier kernels
   const int* prefix = p.tile_prefix;
+  if constexpr (kShared) {
+    if (p.fold) {  // its scratch lies in the P buffer, which no tile uses yet
+      using Scratch = shared::PlanScratch<kThreads, kThreads>;
+      static_assert(sizeof(Scratch) <= 2 * kChunk && kTile == shared::kPlanTile, "plan scratch");
+      shared::make_plan<kThreads>(p.plan, *reinterpret_cast<Scratch*>(data + kPOff), cluster == 0 && rank == 0);
+      __syncthreads();
+    }
+  }
   int4 start_at = make_int4(0, 0, 0, 0);
   if constexpr (kShared) start_at = p.start[cluster];
   const bool has_work = [&] {

@@ -558,7 +558,7 @@ bool shared_packs(const mla_dims* d, int B, long P) {
   if (P == 0 || B < 2) return false;
   if (!shared_tc_eligible(d)) return decode_mma_eligible(d);
   const long R = (long)B * d->n_heads, Mt = (R + 127) / 128;
-  return B * tiles_of(P) - Mt * (tiles_of(P) + tc::kItemUnits) > 16 + R / 48;
+  return B * tiles_of(P) - Mt * (tiles_of(P) + shared::kItemUnits) > 16 + R / 48;
 }
 // Whether some prefix makes the call pack (its workspace then has room for it).
 bool shared_may_pack(const mla_dims* d, int B) { return ((long)B * d->n_heads + 127) / 128 < B; }
@@ -635,6 +635,23 @@ size_t ws_shared(const mla_dims* d, int B, int max_seq_len) {
 // into 37 parts each, one into 74.
 constexpr unsigned kMergeFewRows = 256, kMergeManyRows = 2048;
 
+// As many threads of a plan to a sequence as the block has for B of them.
+int plan_lanes(int B, int threads) {
+  int lanes = 1;
+  while (lanes < 32 && 2 * lanes * B <= threads) lanes *= 2;
+  return lanes;
+}
+
+// Whether the attention kernel's CTAs make the plan themselves, each the whole of it: a launch less,
+// and about as long on the device as the plan kernel, while there are few sequences (a thread has
+// one) and few page ids to check. Measured, us folded / with the plan kernel: 4 sequences of 16 heads
+// behind 512 tokens 20.2 / 22.3 a call from Python, 18.1 / 18.5 on the device; 64 of 128 heads, 4224
+// page ids 94 / 94; 4 of 128 heads, 8196 ids 167.5 / 167.9; 64 of 128 heads, 32832 ids 548 / 540.
+bool shared_folds(const shared::PlanArgs& a) {
+  const long own = a.max_seq_len - (long)a.n_shared * a.page_size;
+  return a.B <= 256 && a.B * ((own + a.page_size - 1) / a.page_size) <= 8192;
+}
+
 template <typename T>
 int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_pages, shared::PlanArgs& plan,
                    void* o_lat, float* lse_out, char* ws, cudaStream_t st, int32_t& launches) {
@@ -672,8 +689,15 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
   if (own_q_rows > 0)
     ok = ok && host::encode_chunks(&maps.q1, q, bf16, (uint64_t)B * n_h, tc::dec::kD * 2, 1, (uint32_t)own_q_rows);
   if (!ok) return MLA_ERR_CUDA;
-  if (launch_pdl(k_shared_plan, dim3(1), dim3(1024), 0, st, plan) != cudaSuccess) return MLA_ERR_CUDA;
+  const bool fold = shared_folds(plan);
+  plan.lanes = plan_lanes(B, fold ? tc::dec::kThreads : 1024);
+  if (!fold) {
+    if (launch_pdl(k_shared_plan, dim3(1), dim3(1024), 0, st, plan) != cudaSuccess) return MLA_ERR_CUDA;
+    ++launches;
+  }
   tc::SharedTcParams p;
+  p.fold = fold ? 1 : 0;
+  p.plan = plan;
   p.bt = plan.bt;
   p.max_pages = plan.max_pages;
   p.seq_lens = plan.len;
@@ -708,7 +732,7 @@ int shared_tc_impl(const mla_dims* d, const void* q, const void* pool, int32_t n
       : R <= kMergeManyRows ? launch_pdl(k_shared_merge<T, 64, 1>, dim3((R + 1) / 2), dim3(128), 0, st, m)
                             : launch_pdl(k_shared_merge<T, 32, 1>, dim3((R + 3) / 4), dim3(128), 0, st, m);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
-  launches += 3;
+  launches += 2;
   return MLA_OK;
 }
 
@@ -803,8 +827,7 @@ int shared_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_
   plan.shared_pages = shared_pages;
   const bool tc_path = shared_tc_eligible(d), mma_path = decode_mma_eligible(d);
   plan.n_shared = shared_packs(d, B, (long)num_shared * d->page_size) ? num_shared : 0;
-  plan.lanes = 1;  // as many threads to a sequence as the block has for B of them
-  while (plan.lanes < 32 && 2 * plan.lanes * B <= 1024) plan.lanes *= 2;
+  plan.lanes = plan_lanes(B, 1024);
   int32_t n = 0;
   int r;
   if (tc_path) {
@@ -1199,7 +1222,7 @@ int mla_shared_prefix_attention(const mla_dims* dims, const void* q, const void*
   if (num_shared_pages < 0 || (long)num_shared_pages * dims->page_size > (long)max_seq_len) return MLA_ERR_INVALID_ARG;
   // the places of all items in the attention kernel's list stay in int32: a packed row tile and a
   // sequence take at most two more than the pages of a longest sequence
-  if (2L * B * (pages_of(dims, max_seq_len) + tc::kItemUnits) > (long)INT32_MAX) return MLA_ERR_INVALID_ARG;
+  if (2L * B * (pages_of(dims, max_seq_len) + shared::kItemUnits) > (long)INT32_MAX) return MLA_ERR_INVALID_ARG;
   if (B == 0) {
     t_launches[MLA_CALL_SHARED_PREFIX_ATTENTION] = 0;
     return MLA_OK;

@@ -15,170 +15,13 @@
 
 namespace mla {
 
-namespace shared {
-constexpr int kScanSeqs = 4096;  // sequences whose tile counts the plan keeps in shared memory
-
-struct PlanArgs {
-  const int* seq_lens;  // [B]
-  const int* bt;        // [B, max_pages]
-  int B, max_pages, num_pages, max_seq_len, page_size;
-  const int* shared_pages;
-  int n_shared;      // pages of the prefix; 0: no sequence has a shared part
-  int lanes;         // threads that check one sequence's pages (a power of two <= 32)
-  int prefix_items;  // packed row tiles
-  int* first;        // [B] first token of the sequence's own part, -1 for a rejected sequence
-  int* len;          // [B] its length, 0 for a rejected sequence
-  int* tile_prefix;  // [prefix_items + B + 1] places before each item in the list of the items'
-                     // tiles, kItemUnits places and then its tiles to an item that has any; or null
-  int* pairs;        // [prefix_items + B] first and last pair of an item's tiles, c0 | c1 << 16, -1: none
-  int4* start;       // [C] item that each pair begins in, its places [y, z), all places
-  int C;             // pairs
-};
-}  // namespace shared
-
-// One block of 1024 threads: checks the shared pages and every sequence's length and own pages,
-// gives each sequence its own part, and (tile_prefix) lists the tiles of all items: the packed row
-// tiles first, each over the whole prefix, then the sequences. A sequence shorter than the prefix
-// (an idle row of a padded batch) attends to its own tokens alone. Rejected sequences have no
-// tiles; their output becomes zeros. The host keeps the tile total within int32.
+// The plan as a kernel of its own: one block. Calls with few sequences run it in every CTA of the
+// attention kernel instead (see shared_folds in libmla.cu).
 __global__ void __launch_bounds__(1024) k_shared_plan(const shared::PlanArgs a) {
-  __shared__ int s_count[shared::kScanSeqs];
-  __shared__ int warp_total[32];
-  __shared__ int s_run[1024];
+  __shared__ shared::PlanScratch<1024, shared::kScanSeqs> scratch;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int P = a.page_size, shared_len = a.n_shared * P;
-  // the first sequence's length, and the page it then most likely asks for first, are requested
-  // beside the shared pages
-  const int per_pass = 1024 / a.lanes, sub = tid & (a.lanes - 1);
-  const int b_first = tid / a.lanes, t_first = a.n_shared + sub;
-  const int L_first = b_first < a.B ? a.seq_lens[b_first] : 0;
-  const int pg_first = b_first < a.B && t_first < a.max_pages ? a.bt[(long)b_first * a.max_pages + t_first] : 0;
-  bool bad = false;
-  for (int t = tid; t < a.n_shared; t += 1024) {
-    const int pg = a.shared_pages[t];
-    bad |= pg < 0 || pg >= a.num_pages;
-  }
-  const bool bad_prefix = __syncthreads_or(bad);
-  for (int b0 = 0; b0 < a.B; b0 += per_pass) {
-    const int b = b0 + b_first;
-    int L = 0, n = 0, f = 0;
-    bool len_ok = false;
-    if (b < a.B) {
-      L = b0 == 0 ? L_first : a.seq_lens[b];
-      len_ok = L >= 1 && L <= a.max_seq_len;
-      n = len_ok ? (L - 1) / P + 1 : 0;
-      len_ok = len_ok && n <= a.max_pages;
-      f = len_ok && shared_len > 0 && L >= shared_len ? shared_len : 0;
-    }
-    bad = false;
-    if (len_ok) {
-      const int* row = a.bt + (long)b * a.max_pages;
-      int t = f / P + sub;
-      if (b0 == 0 && t == t_first && t < n) {
-        bad |= pg_first < 0 || pg_first >= a.num_pages;
-        t += a.lanes;
-      }
-#pragma unroll 4
-      for (; t < n; t += a.lanes) {
-        const int pg = row[t];
-        bad |= pg < 0 || pg >= a.num_pages;
-      }
-    }
-    for (int o = 1; o < a.lanes; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
-    bad |= f > 0 && bad_prefix;
-    if (b < a.B && sub == 0) {
-      if (!len_ok) record_error(MLA_ERR_BAD_SEQ_LEN);
-      else if (bad) record_error(MLA_ERR_BAD_PAGE);
-      const bool ok = len_ok && !bad;
-      a.first[b] = ok ? f : -1;
-      a.len[b] = ok ? L : 0;
-      if (a.tile_prefix != nullptr) {
-        const int tiles = ok && L > f ? tc::kItemUnits + (L - f + tc::dec::kTile - 1) / tc::dec::kTile : 0;
-        if (a.B <= shared::kScanSeqs) s_count[b] = tiles;
-        else a.tile_prefix[a.prefix_items + b] = tiles;
-      }
-    }
-  }
-  if (a.tile_prefix == nullptr) return;
-  const int nt = bad_prefix || shared_len == 0 ? 0 : tc::kItemUnits + (shared_len + tc::dec::kTile - 1) / tc::dec::kTile;
-  int* const mine = a.tile_prefix + a.prefix_items;
-  for (int i = tid; i < a.prefix_items; i += 1024) a.tile_prefix[i] = i * nt;
-  __syncthreads();
-  const int* const count = a.B <= shared::kScanSeqs ? s_count : mine;
-  // exclusive scan: thread tid sums `per` sequences, then a two-level shuffle scan of the sums
-  const int per = (a.B + 1023) / 1024;
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += count[b];
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) warp_total[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    int w = warp_total[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += v;
-    }
-    warp_total[lane] = w;
-  }
-  __syncthreads();
-  const long T = (long)a.prefix_items * nt + warp_total[31];
-  const bool narrow = T < (1u << 31) / tc::kMaxDecodeClusters;  // a pair's number fits 32-bit arithmetic
-  auto pair_of = [&](int g) {
-    return narrow ? (int)(((unsigned)(g + 1) * (unsigned)a.C - 1u) / (unsigned)T) : tc::cluster_of(g, T, a.C);
-  };
-  auto pairs_of = [&](int begin, int n) {
-    if (n == 0) return -1;
-    return pair_of(begin + tc::kItemUnits) | (pair_of(begin + n - 1) << 16);
-  };
-  for (int i = tid; i < a.prefix_items; i += 1024) a.pairs[i] = pairs_of(i * nt, nt);
-  s_run[tid] = a.prefix_items * nt + incl - sum + (warp > 0 ? warp_total[warp - 1] : 0);
-  int run = s_run[tid];
-  for (int b = b0; b < b1; ++b) {
-    const int n = count[b];  // read before the same place may be overwritten
-    mine[b] = run;
-    a.pairs[a.prefix_items + b] = pairs_of(run, n);
-    run += n;
-  }
-  if (tid == 1023) mine[a.B] = (int)T;
-  __syncthreads();
-  if (tid < a.C) {                  // the item that pair tid begins in
-    const int g = narrow ? (int)((unsigned)T * (unsigned)tid / (unsigned)a.C) : (int)(T * tid / a.C);
-    int item, base, next;
-    if (g < a.prefix_items * nt) {
-      item = g / nt;
-      base = item * nt;
-      next = base + nt;
-    } else {
-      int lo = 0, hi = 1023;  // the last thread whose sequences begin at or before g
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_run[mid] <= g) lo = mid; else hi = mid - 1;
-      }
-      // (threads past the last sequence hold the total, which only a list without places reaches)
-      int b = min(lo * per, a.B - 1);
-      base = s_run[lo];
-      if (per == 1) {
-        next = b + 1 < a.B ? s_run[b + 1] : (int)T;
-      } else {
-        while (b + 1 < a.B && (next = mine[b + 1]) <= g) {
-          ++b;
-          base = next;
-        }
-        if (b + 1 == a.B) next = (int)T;
-      }
-      item = a.prefix_items + b;
-    }
-    a.start[tid] = make_int4(item, base, next, (int)T);
-  }
+  shared::make_plan<1024>(a, scratch, true);
 }
 
 namespace shared {
@@ -202,7 +45,7 @@ struct Parts {
     if (pairs < 0) return;
     n = (pairs >> 16) - (pairs & 0xffff) + 1;
     if (!dense) {
-      g0 = prefix[0] + tc::kItemUnits;
+      g0 = prefix[0] + kItemUnits;
       n = prefix[1] - g0;
     }
   }

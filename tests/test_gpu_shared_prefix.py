@@ -168,6 +168,20 @@ def test_many_sequences(d, B):
     assert float((lse - ref_l).abs().max()) < 2.0 ** -8
 
 
+@pytest.mark.parametrize("heads,B,shared,longest", [(16, 300, 4, 0), (128, 40, 2, 40000), (16, 40, 8, 40000)])
+def test_plan_as_a_kernel_of_its_own(heads, B, shared, longest):
+    """Many sequences, or a bound on their lengths that allows many pages: three launches instead of two."""
+    d = P.with_(n_heads=heads)
+    c = Case(d, batch(B, shared * d.page_size, EDGES), shared, seed=15, spare=650 if longest else 1)
+    o, lse = c.run()
+    few = M.last_launch_count(M.CALL_SHARED_PREFIX_ATTENTION)
+    c.check(o, lse)
+    o, lse = c.run(longest=longest or c.longest)
+    assert M.read_device_status() == 0
+    assert M.last_launch_count(M.CALL_SHARED_PREFIX_ATTENTION) == 3 and few == (2 if longest else 3)
+    c.check(o, lse)
+
+
 @pytest.mark.parametrize("d", [P.with_(n_heads=16), P.with_(n_heads=48), P, R], ids=["h16", "h48", "h128", "narrow"])
 def test_agrees_with_decode_and_repeats_bitwise(d):
     lens = batch(24, 40 * d.page_size, [1, 500, 64, 1000])
