@@ -295,8 +295,8 @@ int mla_decode_attention_fp8(const mla_dims* dims, const void* q, const void* po
  *   k' = k^ / sqrt(mean(k^^2) + eps) * gain_r (k' = k^ if gain_r is NULL);  k^R = RoPE(k', pos[t])
  *   pool row of (seq_idx[t], pos[t]), as in mla_append_kv  <-  [c' ‖ k^R] rounded to the element type.
  * Everything between x and the row is fp32 (angles in double). x_stride >= d_c + d_rope, a
- * multiple of 8; gain_c [d_c] and gain_r [d_rope] in the element type; eps > 0 and finite where a
- * gain is given (MLA_ERR_INVALID_ARG otherwise). Any dims of mla_check_dims, one launch, no
+ * multiple of 8; gain_c [d_c] and gain_r [d_rope] in the element type; eps > 0 and finite in fp32
+ * where a gain is given (MLA_ERR_INVALID_ARG otherwise). Any dims of mla_check_dims, one launch, no
  * workspace. A token whose slot is outside the table or the pool is not written and records
  * MLA_ERR_BAD_PAGE; slots of no token are left as they are. No two tokens of one call may have the
  * same slot (which of them it holds, or parts of which, is not defined). 0 <= T <= 2^30

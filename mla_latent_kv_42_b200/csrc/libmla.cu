@@ -497,7 +497,8 @@ int norm_append_call(const mla_dims* d, const void* x, int64_t x_stride, const v
   if (r != MLA_OK) return r;
   if (T < 0 || T > kMaxRowTokens || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return MLA_ERR_INVALID_ARG;
   if (x_stride < d->d_c + d->d_rope || x_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
-  if ((g_c || g_r) && !(eps > 0.0 && std::isfinite(eps))) return MLA_ERR_INVALID_ARG;
+  const float eps32 = (float)eps;  // as the kernel uses it
+  if ((g_c || g_r) && !(eps32 > 0.f && std::isfinite(eps32))) return MLA_ERR_INVALID_ARG;
   if (T == 0) {
     t_launches[kFp8 ? MLA_CALL_NORM_APPEND_KV_FP8 : MLA_CALL_NORM_APPEND_KV] = 0;
     return MLA_OK;

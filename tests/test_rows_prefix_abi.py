@@ -44,6 +44,18 @@ def test_norm_append_refusals(lib, name, d):
     assert f(*swap(args, _0=ctypes.byref(bad))) == -2 and f(*swap(args, _0=None)) == -1
 
 
+@pytest.mark.parametrize("name", ["mla_norm_append_kv", "mla_norm_append_kv_fp8"])
+@pytest.mark.parametrize("eps", [1e-50, 1e300])
+def test_norm_append_eps_outside_fp32(lib, name, eps):
+    """0 or infinity in fp32, where the rows are normalised: a row of zeros would become NaN, any row zeros."""
+    d = synth.PRODUCTION
+    cd = M.c_dims(d)
+    # T, x and pool as in a good call, the misaligned x keeps an accepted eps from being launched
+    args = [ctypes.byref(cd), MISALIGNED, d.D, FAKE, FAKE, eps, FAKE, FAKE, FAKE, 2, 4, FAKE, 10, 3, None]
+    assert getattr(lib, name)(*args) == -1
+    assert getattr(lib, name)(*swap(args, _3=None, _4=None)) == -4  # eps is not used
+
+
 @pytest.mark.parametrize("name", ["mla_read_kv", "mla_read_kv_fp8"])
 def test_read_refusals(lib, name):
     d = synth.PRODUCTION
