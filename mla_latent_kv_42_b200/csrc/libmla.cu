@@ -643,11 +643,13 @@ int plan_lanes(int B, int threads) {
   return lanes;
 }
 
-// Whether the attention kernel's CTAs make the plan themselves, each the whole of it: a launch less,
-// and about as long on the device as the plan kernel, while there are few sequences (a thread has
-// one) and few page ids to check. Measured, us folded / with the plan kernel: 4 sequences of 16 heads
-// behind 512 tokens 20.2 / 22.3 a call from Python, 18.1 / 18.5 on the device; 64 of 128 heads, 4224
-// page ids 94 / 94; 4 of 128 heads, 8196 ids 167.5 / 167.9; 64 of 128 heads, 32832 ids 548 / 540.
+// Whether the attention kernel's CTAs make the plan themselves, each the whole of it: a launch less
+// while there are few sequences (a thread has one) and few page ids to check. Measured on the device,
+// us folded / with the plan kernel: 4 sequences of 16 heads behind 512 tokens 18.2 / 19.1 (a call from
+// Python 20.1 to 21.8 / 22.4 to 24.0), 64 behind 512 24.8 / 26.1; 23 of 64 heads behind 4096
+// 35.4 / 36.0, 64 of 128 heads 94.0 / 95.0. The other way, by less than 1%: 64 of 16 heads behind
+// 8192 47.5 / 47.3, 128 behind 8192 66.5 / 66.1, 200 of 32 heads 144.9 / 144.1. By the ids: 4 of 128
+// heads, 8196 of them, 167.5 / 167.9; 64 of 128 heads, 32832 of them, 548 / 540.
 bool shared_folds(const shared::PlanArgs& a) {
   const long own = a.max_seq_len - (long)a.n_shared * a.page_size;
   return a.B <= 256 && a.B * ((own + a.page_size - 1) / a.page_size) <= 8192;
