@@ -4,6 +4,10 @@ Argument marshalling only: every step of the path runs in libmla's CUDA kernels,
 through the C ABI of ``include/mla.h``. Torch supplies device memory and streams. If the
 shared library is missing, every call raises; there is no fallback of any kind.
 
+A call given a ``stream`` is queued there and takes the outputs and workspaces that the caller did
+not pass from that stream's memory, so that they may be used at once; that the inputs are ready
+there, and the outputs are not read before, is the caller's to order (``wait_stream``, events).
+
 Method: "DeepSeek-V2 from Scratch", §6 (the complete MLA algorithm) in the absorbed form of
 §5.3: append the new token's latent row, absorb W^UK into the query, attend in latent space,
 fold W^UV into the output projection.
@@ -173,11 +177,31 @@ def cache_elems_per_token(dims) -> int:
     return int(_lib().mla_cache_elems_per_token(ctypes.byref(cd)))
 
 
-def _ws(dims, call, B, max_seq_len, ws, device):
+def _own(stream, like, shape, dtype):
+    """A tensor of a call's own on the device of ``like``, from the memory of the stream that the call
+    runs on: what another stream's tensors have freed may still be in use there."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _out(stream, like, shape, dtype):
+    """The same for an output, which the caller's current stream may read: once freed it is also kept
+    from reuse until that stream is through with what it has queued by then."""
+    t = _own(stream, like, shape, dtype)
+    if stream is not None:
+        import torch
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _ws(dims, call, B, max_seq_len, ws, stream, like):
     import torch
     n = workspace_size(dims, call, B, max_seq_len)
     if ws is None:
-        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+        ws = _own(stream, like, max(n, 16), torch.uint8)
     return ws, ws.numel() * ws.element_size()
 
 
@@ -189,7 +213,7 @@ def append_kv(dims, h, w_dkv_kr, seq_idx, pos, block_table, pool, ws=None, strea
                      (pos, "pos", torch.int32), (block_table, "block_table", torch.int32), (pool, "pool", e)):
         _need(t, dt, n)
     T = h.shape[0]
-    ws, nbytes = _ws(dims, CALL_APPEND_KV, T, 0, ws, h.device)
+    ws, nbytes = _ws(dims, CALL_APPEND_KV, T, 0, ws, stream, h)
     cd = c_dims(dims)
     _check(_lib().mla_append_kv(ctypes.byref(cd), _ptr(h), _ptr(w_dkv_kr), _ptr(seq_idx), _ptr(pos),
                                 _ptr(block_table), block_table.shape[0], block_table.shape[1], _ptr(pool),
@@ -206,9 +230,9 @@ def absorb_query(dims, h, w_dq, w_uq_qr, w_uk, pos, q_out=None, ws=None, stream=
         _need(t, dt, n)
     B = h.shape[0]
     if q_out is None:
-        q_out = torch.empty((B, dims.n_heads, dims.d_c + dims.d_rope), dtype=e, device=h.device)
+        q_out = _out(stream, h, (B, dims.n_heads, dims.d_c + dims.d_rope), e)
     _need(q_out, e, "q_out")
-    ws, nbytes = _ws(dims, CALL_ABSORB_QUERY, B, 0, ws, h.device)
+    ws, nbytes = _ws(dims, CALL_ABSORB_QUERY, B, 0, ws, stream, h)
     cd = c_dims(dims)
     _check(_lib().mla_absorb_query(ctypes.byref(cd), _ptr(h), _ptr(w_dq), _ptr(w_uq_qr), _ptr(w_uk), _ptr(pos),
                                    _ptr(q_out), B, _ptr(ws), nbytes, _stream(stream)), "mla_absorb_query")
@@ -225,13 +249,13 @@ def decode_attention(dims, q, pool, block_table, seq_lens, max_seq_len, o_lat=No
         _need(t, dt, n)
     B = q.shape[0]
     if o_lat is None:
-        o_lat = torch.empty((B, dims.n_heads, dims.d_c), dtype=e, device=q.device)
+        o_lat = _out(stream, q, (B, dims.n_heads, dims.d_c), e)
     if lse is None and want_lse:
-        lse = torch.empty((B, dims.n_heads), dtype=torch.float32, device=q.device)
+        lse = _out(stream, q, (B, dims.n_heads), torch.float32)
     _need(o_lat, e, "o_lat")
     if lse is not None:
         _need(lse, torch.float32, "lse")
-    ws, nbytes = _ws(dims, CALL_DECODE_ATTENTION, B, max_seq_len, ws, q.device)
+    ws, nbytes = _ws(dims, CALL_DECODE_ATTENTION, B, max_seq_len, ws, stream, q)
     cd = c_dims(dims)
     _check(_lib().mla_decode_attention(ctypes.byref(cd), _ptr(q), _ptr(pool), pool.shape[0], _ptr(block_table),
                                        block_table.shape[1], _ptr(seq_lens), B, int(max_seq_len), _ptr(o_lat),
@@ -262,7 +286,7 @@ def append_kv_fp8(dims, h, w_dkv_kr, seq_idx, pos, block_table, pool, ws=None, s
     if pool.dim() != 2 or pool.shape[1] != fp8_page_bytes(dims):
         raise ValueError("pool must be uint8 [num_pages, fp8_page_bytes(dims)]")
     T = h.shape[0]
-    ws, nbytes = _ws(dims, CALL_APPEND_KV_FP8, T, 0, ws, h.device)
+    ws, nbytes = _ws(dims, CALL_APPEND_KV_FP8, T, 0, ws, stream, h)
     cd = c_dims(dims)
     _check(_lib().mla_append_kv_fp8(ctypes.byref(cd), _ptr(h), _ptr(w_dkv_kr), _ptr(seq_idx), _ptr(pos),
                                     _ptr(block_table), block_table.shape[0], block_table.shape[1], _ptr(pool),
@@ -283,13 +307,13 @@ def decode_attention_fp8(dims, q, pool, block_table, seq_lens, max_seq_len, o_la
         raise ValueError("pool must be uint8 [num_pages, fp8_page_bytes(dims)]")
     B = q.shape[0]
     if o_lat is None:
-        o_lat = torch.empty((B, dims.n_heads, dims.d_c), dtype=e, device=q.device)
+        o_lat = _out(stream, q, (B, dims.n_heads, dims.d_c), e)
     if lse is None and want_lse:
-        lse = torch.empty((B, dims.n_heads), dtype=torch.float32, device=q.device)
+        lse = _out(stream, q, (B, dims.n_heads), torch.float32)
     _need(o_lat, e, "o_lat")
     if lse is not None:
         _need(lse, torch.float32, "lse")
-    ws, nbytes = _ws(dims, CALL_DECODE_ATTENTION_FP8, B, max_seq_len, ws, q.device)
+    ws, nbytes = _ws(dims, CALL_DECODE_ATTENTION_FP8, B, max_seq_len, ws, stream, q)
     cd = c_dims(dims)
     _check(_lib().mla_decode_attention_fp8(ctypes.byref(cd), _ptr(q), _ptr(pool), pool.shape[0], _ptr(block_table),
                                            block_table.shape[1], _ptr(seq_lens), B, int(max_seq_len), _ptr(o_lat),
@@ -311,13 +335,13 @@ def prefill_attention(dims, q, pool, block_table, seq_idx, pos, max_seq_len, o_l
         _need(t, dt, n)
     T = q.shape[0]
     if o_lat is None:
-        o_lat = torch.empty((T, dims.n_heads, dims.d_c), dtype=e, device=q.device)
+        o_lat = _out(stream, q, (T, dims.n_heads, dims.d_c), e)
     if lse is None and want_lse:
-        lse = torch.empty((T, dims.n_heads), dtype=torch.float32, device=q.device)
+        lse = _out(stream, q, (T, dims.n_heads), torch.float32)
     _need(o_lat, e, "o_lat")
     if lse is not None:
         _need(lse, torch.float32, "lse")
-    ws, nbytes = _ws(dims, CALL_PREFILL_ATTENTION, T, max_seq_len, ws, q.device)
+    ws, nbytes = _ws(dims, CALL_PREFILL_ATTENTION, T, max_seq_len, ws, stream, q)
     cd = c_dims(dims)
     _check(_lib().mla_prefill_attention(ctypes.byref(cd), _ptr(q), _ptr(pool), pool.shape[0], _ptr(block_table),
                                         block_table.shape[0], block_table.shape[1], _ptr(seq_idx), _ptr(pos), T,
@@ -342,9 +366,9 @@ def decode_attention_noalloc(dims, q, pool, block_table, seq_lens, max_seq_len, 
         _need(t, dt, n)
     B = q.shape[0]
     if o_lat is None:
-        o_lat = torch.empty((B, dims.n_heads, dims.d_c), dtype=e, device=q.device)
+        o_lat = _out(stream, q, (B, dims.n_heads, dims.d_c), e)
     if lse is None and want_lse:
-        lse = torch.empty((B, dims.n_heads), dtype=torch.float32, device=q.device)
+        lse = _out(stream, q, (B, dims.n_heads), torch.float32)
     _need(o_lat, e, "o_lat")
     if lse is not None:
         _need(lse, torch.float32, "lse")
@@ -358,15 +382,14 @@ def decode_attention_noalloc(dims, q, pool, block_table, seq_lens, max_seq_len, 
 
 def out_proj(dims, o_lat, w_uv, w_o, u=None, ws=None, stream=None):
     """mla_out_proj: u = W^O [W^UV_1 o_lat_1; ...; W^UV_n_h o_lat_n_h]."""
-    import torch
     e = _elem(dims)
     for t, n in ((o_lat, "o_lat"), (w_uv, "w_uv"), (w_o, "w_o")):
         _need(t, e, n)
     B = o_lat.shape[0]
     if u is None:
-        u = torch.empty((B, dims.d_model), dtype=e, device=o_lat.device)
+        u = _out(stream, o_lat, (B, dims.d_model), e)
     _need(u, e, "u")
-    ws, nbytes = _ws(dims, CALL_OUT_PROJ, B, 0, ws, o_lat.device)
+    ws, nbytes = _ws(dims, CALL_OUT_PROJ, B, 0, ws, stream, o_lat)
     cd = c_dims(dims)
     _check(_lib().mla_out_proj(ctypes.byref(cd), _ptr(o_lat), _ptr(w_uv), _ptr(w_o), _ptr(u), B, _ptr(ws), nbytes,
                                _stream(stream)), "mla_out_proj")
@@ -416,13 +439,6 @@ def _pool_shape(dims, pool, fp8):
     D = dims.d_c + dims.d_rope
     n = pool.shape[0] if pool.dim() else 0
     return (n, dims.page_size * (D + 8)) if fp8 else (n, dims.page_size, D)
-
-
-def _on(stream, t):
-    """A tensor of this call's own, kept from reuse until the stream it is used on is through with it."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def _raw_stream(torch, here, stream):
@@ -481,7 +497,7 @@ def _read(fn, name, fp8, dims, pool, seq_idx, pos, block_table, out, stream):
                 (block_table, "block_table", i32, (S, width)),
                 *([] if out is None else [(out, "out", e, (T, D))]), strided="out")
     if out is None:
-        out = _on(stream, pool.new_empty((T, D), dtype=e))
+        out = _out(stream, pool, (T, D), e)
     code = fn(ctypes.byref(c_dims(dims)), pool.data_ptr(), shape[0], seq_idx.data_ptr(), pos.data_ptr(),
               block_table.data_ptr(), S, width, out.data_ptr(), out.stride(0) if T > 1 else D, T,
               _raw_stream(torch, here, stream))
@@ -523,13 +539,13 @@ def shared_prefix_attention(dims, q, pool, block_table, seq_lens, max_seq_len, s
                 *([] if lse is None else [(lse, "lse", torch.float32, (B, H))]),
                 *([] if ws is None else [(ws, "ws", ws.dtype, ws.shape)]))
     if o_lat is None:
-        o_lat = _on(stream, q.new_empty((B, H, dims.d_c)))
+        o_lat = _out(stream, q, (B, H, dims.d_c), e)
     if lse is None and want_lse:
-        lse = _on(stream, q.new_empty((B, H), dtype=torch.float32))
+        lse = _out(stream, q, (B, H), torch.float32)
     lib, cd = _lib(), ctypes.byref(c_dims(dims))
     if ws is None:
         n = lib.mla_workspace_size(cd, CALL_SHARED_PREFIX_ATTENTION, B, max_seq_len)
-        ws = _on(stream, q.new_empty(max(n, 16), dtype=torch.uint8))
+        ws = _own(stream, q, max(n, 16), torch.uint8)
     code = lib.mla_shared_prefix_attention(
         cd, q.data_ptr(), pool.data_ptr(), shape[0], block_table.data_ptr(), width, seq_lens.data_ptr(), B,
         max_seq_len, shared_pages.data_ptr(), n_shared, o_lat.data_ptr(), None if lse is None else lse.data_ptr(),
@@ -606,20 +622,19 @@ def layer_step_small(st: LayerState, h, seq_lens, max_seq_len, ws=None, out=None
     out = out or {}
     e = _elem(d)
     B = h.shape[0]
-    dev = h.device
     q = out.get("q")
     if q is None:
-        q = torch.empty((B, d.n_heads, d.d_c + d.d_rope), dtype=e, device=dev)
+        q = _out(stream, h, (B, d.n_heads, d.d_c + d.d_rope), e)
     o_lat = out.get("o_lat")
     if o_lat is None:
-        o_lat = torch.empty((B, d.n_heads, d.d_c), dtype=e, device=dev)
+        o_lat = _out(stream, h, (B, d.n_heads, d.d_c), e)
     lse = out.get("lse")
     if lse is None and out.get("want_lse", True):
-        lse = torch.empty((B, d.n_heads), dtype=torch.float32, device=dev)
+        lse = _out(stream, h, (B, d.n_heads), torch.float32)
     u = out.get("u")
     if u is None:
-        u = torch.empty((B, d.d_model), dtype=e, device=dev)
-    ws, nbytes = _ws(d, CALL_LAYER_STEP_SMALL, B, max_seq_len, ws, dev)
+        u = _out(stream, h, (B, d.d_model), e)
+    ws, nbytes = _ws(d, CALL_LAYER_STEP_SMALL, B, max_seq_len, ws, stream, h)
     cd = c_dims(d)
     pool, bt = st.pool, st.block_table
     _check(_lib().mla_layer_step_small(ctypes.byref(cd), _ptr(h), _ptr(w["w_dkv_kr"]), _ptr(w["w_dq"]),
