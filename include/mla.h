@@ -345,8 +345,9 @@ int mla_read_kv_fp8(const mla_dims* dims, const void* pool, int32_t num_pages, c
  * shared_pages int32 [num_shared_pages]: the pages of the first num_shared_pages * page_size
  * tokens (0: nothing is shared; at most max_seq_len tokens, MLA_ERR_INVALID_ARG otherwise). Every
  * sequence at least that long begins with these pages, and its block-table row lists them too (the
- * call reads them from either place). A sequence that is shorter, such as an idle row of a padded
- * batch, attends to the seq_lens[b] tokens of its own row alone.
+ * call reads them from either place; ids in shared_pages are always checked, the row's where they
+ * are read). A sequence that is shorter, such as an idle row of a padded batch, attends to the
+ * seq_lens[b] tokens of its own row alone.
  * The other arguments, limits and outputs as mla_decode_attention; 2 B (pages of max_seq_len + 2)
  * must stay below 2^31. lse_out is good to fp32 where d_c = 512, d_rope = 64 and
  * page_size = 64 or where the shape meets mla_layer_step_small's limits on heads, widths and pages:

@@ -828,6 +828,7 @@ int shared_impl(const mla_dims* d, const void* q, const void* pool, int32_t num_
   plan.max_seq_len = max_seq_len;
   plan.page_size = d->page_size;
   plan.shared_pages = shared_pages;
+  plan.n_given = num_shared;
   const bool tc_path = shared_tc_eligible(d), mma_path = decode_mma_eligible(d);
   plan.n_shared = shared_packs(d, B, (long)num_shared * d->page_size) ? num_shared : 0;
   plan.lanes = plan_lanes(B, 1024);

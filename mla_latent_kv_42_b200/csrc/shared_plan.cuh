@@ -21,7 +21,8 @@ struct PlanArgs {
   const int* bt;        // [B, max_pages]
   int B, max_pages, num_pages, max_seq_len, page_size;
   const int* shared_pages;
-  int n_shared;      // pages of the prefix; 0: no sequence has a shared part
+  int n_given;       // pages of the prefix: a bad one rejects every sequence that has them
+  int n_shared;      // n_given where rows are packed over the prefix, 0: no sequence has a shared part
   int lanes;         // threads that check one sequence's pages (a power of two <= 32)
   int prefix_items;  // packed row tiles
   int* first;        // [B] first token of the sequence's own part, -1 for a rejected sequence
@@ -61,7 +62,7 @@ __device__ void make_plan(const PlanArgs& a, PlanScratch<kThreads, kCounts>& sc,
   const int pg_first = b_first < a.B && t_first < a.max_pages ? a.bt[(long)b_first * a.max_pages + t_first] : 0;
   if (tid < 32) sc.warp_total[tid] = 0;
   bool bad = false;
-  for (int t = tid; t < a.n_shared; t += kThreads) {
+  for (int t = tid; t < a.n_given; t += kThreads) {
     const int pg = a.shared_pages[t];
     bad |= pg < 0 || pg >= a.num_pages;
   }
@@ -93,7 +94,7 @@ __device__ void make_plan(const PlanArgs& a, PlanScratch<kThreads, kCounts>& sc,
       }
     }
     for (int o = 1; o < a.lanes; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
-    bad |= f > 0 && bad_prefix;
+    bad |= bad_prefix && L >= a.n_given * P;
     if (b < a.B && sub == 0) {
       if (report && !len_ok) record_error(MLA_ERR_BAD_SEQ_LEN);
       else if (report && bad) record_error(MLA_ERR_BAD_PAGE);
