@@ -308,7 +308,7 @@ int mla_norm_append_kv(const mla_dims* dims, const void* x, int64_t x_stride, co
                        mla_stream_t stream);
 
 /* The same into an FP8 cache (the page format above, any dims): s = max|part| / 448 of the fp32
- * parts c' and k^R (1 for an all-zero part), each byte the nearest e4m3 value (ties to even) of
+ * parts c' and k^R (1 where that is zero in fp32), each byte the nearest e4m3 value (ties to even) of
  * value / s in fp32, saturated to +-448. A NaN is stored as NaN and does not enter the maximum; an
  * infinity makes its part's scale infinite, so that the part reads back as NaN. */
 int mla_norm_append_kv_fp8(const mla_dims* dims, const void* x, int64_t x_stride, const void* gain_c,

@@ -214,8 +214,9 @@ __global__ void __launch_bounds__(32 * rows::kWarps, kR == 1 ? rows::kAppendPerS
         if (lane + 32 * j < pairs)
           *reinterpret_cast<P2*>(dst + a.d_c + 2 * (lane + 32 * j)) = Pack<T>::make(r[j].x, r[j].y);
     } else {
-      const float sc = mc > 0.f ? mc / fp8::kE4m3Max : 1.f;
-      const float sr = mr > 0.f ? mr / fp8::kE4m3Max : 1.f;
+      // 1 for an all-zero part, and for one so small (below 2^-141) that fp32 holds its scale as zero
+      const float qc = mc / fp8::kE4m3Max, qr = mr / fp8::kE4m3Max;
+      const float sc = qc > 0.f ? qc : 1.f, sr = qr > 0.f ? qr : 1.f;
       const float ic = 1.f / sc, ir = 1.f / sr;
       // scales whose reciprocal or whose products with values are not normal divide as they are
       const bool plain = !(fminf(sc, sr) > 0x1p-100f && fmaxf(sc, sr) < 0x1p100f);
