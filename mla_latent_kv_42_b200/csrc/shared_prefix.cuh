@@ -230,9 +230,14 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
   const int n_stages = t1 > t0 ? (t1 - t0 + kStageTokens - 1) / kStageTokens : 0;
   const int row_base = tile * shared::kRowTile + 16 * warp;
   const int rows[2] = {row_base + g, row_base + g + 8};
-  bool live[2];  // the row exists and its sequence has this prefix
+  bool live[2];    // the row exists and its sequence has this prefix
+  bool theirs[2];  // another item writes the row's partial
 #pragma unroll
-  for (int e = 0; e < 2; ++e) live[e] = rows[e] < R && g0.first[rows[e] / g0.n_h] > 0;
+  for (int e = 0; e < 2; ++e) {
+    const int b = rows[e] / g0.n_h;
+    live[e] = rows[e] < R && g0.first[b] > 0;
+    theirs[e] = rows[e] >= R || short_has(g0, b, split);
+  }
   const bool warp_live = __any_sync(0xffffffffu, live[0] || live[1]);
 
   uint32_t qa[KDC][4];
@@ -366,7 +371,7 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
       l += __shfl_xor_sync(0xffffffffu, l, o);
       rounded += __shfl_xor_sync(0xffffffffu, rounded, o);
     }
-    if (rows[h2] >= R) continue;
+    if (theirs[h2]) continue;
     const bool some = live[h2] && l != 0.f;  // a NaN goes through
     const float inv = some ? 1.f / rounded : 0.f;
     const long part = (long)rows[h2] * g0.n_splits + split;
@@ -379,19 +384,37 @@ __device__ void prefix_mma_item(const shared::MmaArgs& a, int tile, int split, u
   }
 }
 
-// Blocks [0, row_tiles * pre_splits): prefix items; the rest: (sequence, split) items over own
-// tokens. 128 threads.
+// Blocks [0, row_tiles * pre_splits): prefix items, and then what sequences shorter than the prefix
+// whose first row is the tile's have in the same partial; the rest: (sequence, split) items over
+// own tokens. 128 threads.
 template <typename T, int KDC>
 __global__ void __launch_bounds__(128, 3) k_shared_mma(const shared::MmaArgs a) {
   extern __shared__ __align__(16) uint8_t sm[];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
   const int n_pre = a.row_tiles * a.pre_splits, i = blockIdx.x;
+  int b, b_end, split;
   if (i < n_pre) {
-    prefix_mma_item<T, KDC>(a, i / a.pre_splits, i % a.pre_splits, sm);
+    const int tile = i / a.pre_splits, s = i % a.pre_splits, n_h = a.own.n_h;
+    b = (tile * shared::kRowTile + n_h - 1) / n_h;  // (at most 64 sequences)
+    b_end = min(a.own.B, ((tile + 1) * shared::kRowTile + n_h - 1) / n_h);
+    split = a.own_splits + s;
+    const int mine = b + (int)threadIdx.x;
+    const bool has = mine < b_end && short_has(a.own, mine, s);
+    prefix_mma_item<T, KDC>(a, tile, s, sm);
+    if (!__syncthreads_or(has)) return;
   } else {
     const int j = i - n_pre;
-    attn_mma_item<T, true>(a.own, j / a.own_splits, j % a.own_splits, sm);
+    b = j / a.own_splits;
+    b_end = b + 1;
+    split = j % a.own_splits;
+  }
+  for (; b < b_end; ++b) {
+    if (i < n_pre) {
+      if (!short_has(a.own, b, split - a.own_splits)) continue;  // the same in the whole block
+      __syncthreads();  // shared memory of the item before
+    }
+    attn_mma_item<T, true>(a.own, b, split, sm);
   }
 }
 
