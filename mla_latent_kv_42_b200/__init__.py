@@ -405,7 +405,7 @@ def _ok(t, dtype, shape, here):
 
 def _refuse(here, *named, strided=None):
     """Raise for the first (tensor, name, dtype, shape) that is not on the current device, contiguous (but
-    for the rows of the one called ``strided``), with that type and shape."""
+    for the rows of the one called ``strided``), with that type and shape; always raises."""
     for t, name, dtype, shape in named:
         if t.get_device() < 0:
             raise ValueError(f"{name} must be a CUDA tensor")
@@ -420,6 +420,7 @@ def _refuse(here, *named, strided=None):
                 raise ValueError(f"{name} must be contiguous")
             if t.stride(1) != 1 or t.stride(0) % 8 or t.stride(0) < shape[1]:
                 raise ValueError(f"{name} must be contiguous but for its rows, a multiple of 8 elements apart")
+    raise ValueError("arguments refused: " + ", ".join(f"{name} {tuple(t.shape)} {t.dtype}" for t, name, *_ in named))
 
 
 def _rows_ok(t, dtype, shape, here):
