@@ -294,12 +294,14 @@ int mla_decode_attention_fp8(const mla_dims* dims, const void* q, const void* po
  *   c' = c / sqrt(mean(c^2) + eps) * gain_c   (c' = c if gain_c is NULL)
  *   k' = k^ / sqrt(mean(k^^2) + eps) * gain_r (k' = k^ if gain_r is NULL);  k^R = RoPE(k', pos[t])
  *   pool row of (seq_idx[t], pos[t]), as in mla_append_kv  <-  [c' ‖ k^R] rounded to the element type.
- * Everything between x and the row is fp32 (angles in double). x_stride >= d_c + d_rope, a
- * multiple of 8; gain_c [d_c] and gain_r [d_rope] in the element type; eps > 0 and finite in fp32
- * where a gain is given (MLA_ERR_INVALID_ARG otherwise). Any dims of mla_check_dims, one launch, no
- * workspace. A token whose slot is outside the table or the pool is not written and records
+ * Everything between x and the row is fp32 (angles in double; a part whose sum of squares is past
+ * fp32's range becomes zero). gain_r is for models that normalise the decoupled key too.
+ * x_stride >= d_c + d_rope, a multiple of 8; gain_c [d_c] and gain_r [d_rope] in the element type;
+ * eps > 0 and finite in fp32 where a gain is given (MLA_ERR_INVALID_ARG otherwise). Any dims of
+ * mla_check_dims, one launch, no workspace. A token whose slot is outside the table or the pool is not written and records
  * MLA_ERR_BAD_PAGE; slots of no token are left as they are. No two tokens of one call may have the
- * same slot (which of them it holds, or parts of which, is not defined). 0 <= T <= 2^30
+ * same slot (which of them it holds, or parts of which, is not defined); x must not overlap the
+ * pool. 0 <= T <= 2^30
  * (MLA_ERR_INVALID_ARG otherwise); T == 0 is a no-op.
  */
 int mla_norm_append_kv(const mla_dims* dims, const void* x, int64_t x_stride, const void* gain_c, const void* gain_r,
@@ -310,7 +312,9 @@ int mla_norm_append_kv(const mla_dims* dims, const void* x, int64_t x_stride, co
 /* The same into an FP8 cache (the page format above, any dims): s = max|part| / 448 of the fp32
  * parts c' and k^R (1 where that is zero in fp32), each byte the nearest e4m3 value (ties to even) of
  * value / s in fp32, saturated to +-448. A NaN is stored as NaN and does not enter the maximum; an
- * infinity makes its part's scale infinite, so that the part reads back as NaN. */
+ * infinity makes its part's scale infinite, so that the part reads back as NaN. Attention over such
+ * a cache is mla_decode_attention_fp8 within its dims; elsewhere mla_read_kv_fp8 turns it into pages
+ * that the element-type calls read. */
 int mla_norm_append_kv_fp8(const mla_dims* dims, const void* x, int64_t x_stride, const void* gain_c,
                            const void* gain_r, double eps, const int32_t* seq_idx, const int32_t* pos,
                            const int32_t* block_table, int32_t num_seqs, int32_t max_pages, void* pool,

@@ -482,7 +482,9 @@ int norm_append_impl(const mla_dims* d, const void* x, int64_t x_stride, const v
   double r = std::pow(d->rope_base, -2.0 / (double)d->d_rope);
   for (int j = 0; j < rows::kPowers; ++j, r *= r) a.turns.pw[j] = r;
   const dim3 grid(rows_grid(T_, rows::kAppendPerSm)), block(32 * rows::kWarps);
-  // one pair of the rotated part to a lane where that is enough: the arrays for nine cost registers
+  // one pair of the rotated part to a lane where that is enough: the arrays for nine cost registers and
+  // sines (8192 rows, 16-bit / e4m3: 5.0 / 6.2 us at d_rope = 64, 12.9 / 16.1 at 72 and as much at 568;
+  // arrays for two, which end at 128, 6.5 / 8.1 at 72)
   const cudaError_t e = d->d_rope <= 64 ? launch_pdl(k_norm_append<T, kFp8, 1>, grid, block, 0, st, a)
                                         : launch_pdl(k_norm_append<T, kFp8, rows::kMaxR>, grid, block, 0, st, a);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
@@ -549,10 +551,13 @@ inline long tiles_of(long tokens) { return (tokens + tc::dec::kTile - 1) / tc::d
 // Tensor-core kernel: packing takes ceil(R / 128) items over the prefix in place of its tiles in every
 // sequence. In places of the kernel's list (a place is a tile's time, an item kItemUnits more) that
 // has to save more than the fp32 partials cost that every row then goes through, about a place per
-// 48 rows, and a few places for the further items. Measured on both sides, us packed / unpacked:
-// 16 heads, 4 sequences behind 512 tokens 20.3 / 18.3; 64 behind 128 21.0 / 22.7, 64 of 48 heads
-// behind 512 30.7 / 33.1; 128 of 80 heads behind 1024 84.7 / 83.3, 64 behind 4096 71.2 / 94.5;
-// 64 of 112 heads behind 4096 94.3 / 96.8. From 128 heads up a tile holds one sequence.
+// 48 rows, and a few places for the further items. Measured on both sides, us packed / unpacked, the
+// rule packing: 64 sequences of 16 heads behind 128 tokens 20.4 / 21.7, 64 of 48 behind 512
+// 29.2 / 31.9, 16 of 96 behind 4096 34.8 / 37.1, 64 of 80 69.1 / 91.0, 64 of 112 behind 8192
+// 147.4 / 159.4; not packing: 4 of 16 behind 512 19.5 / 17.8, 128 of 80 behind 1024 63.6 / 61.7, 128 of
+// 96 75.0 / 62.9, 128 of 112 behind 4096 167.3 / 166.2. Near 128 heads it leaves up to 4% there:
+// 64 of 112 behind 4096 89.3 / 93.3 and 64 of 120 behind 8192 158.9 / 161.9 are not packed; a constant
+// that packs them packs 128 of 80 too. From 128 heads up a tile holds one sequence.
 // Narrow rows: packed from two sequences on (8 heads, 2 behind 512 tokens: 12.7 / 13.2; 4 behind
 // 4096: 16.2 / 28.5).
 bool shared_packs(const mla_dims* d, int B, long P) {

@@ -114,3 +114,28 @@ def test_given_tensors_are_used_on_a_side_stream_too():
     got = M.shared_prefix_attention(s.d, s.q, s.pool, s.table, s.lens, s.n, s.shared, o_lat=o, lse=lse, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert got[0] is o and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("name", ["read_kv", "shared", "shared_narrow", "absorb_query"])
+def test_captured_on_a_forked_stream(name):
+    """A call on a stream that a capture forks to, with tensors of its own, replayed with other inputs."""
+    d, call = CALLS[name]
+    s, other, side = State(d, 5), State(d, 6), torch.cuda.Stream()
+    call(s)
+    want = [t.clone() for t in tensors(call(other))]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(2):  # the first one's tensors are freed within the capture
+            got = tensors(call(s, stream=side))
+        torch.cuda.current_stream().wait_stream(side)
+    for a, b in ((s.pool, other.pool), (s.q, other.q), (s.h, other.h), *((s.w[k], other.w[k]) for k in s.w)):
+        a.copy_(b)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert M.read_device_status() == 0
