@@ -13,7 +13,7 @@ constexpr int kMaxPairs = 128;   // pairs at most
 // A pair spends on an item, beside its tiles, the time of about kItemUnits more: its queries'
 // load, the pipeline's fill and the epilogue (a one-tile item took 6.7 us where a tile of a long
 // one takes 2.6). With items counted by tiles alone, 256 one-token sequences behind 32768 shared
-// tokens fell to the last pairs and the call took 1520 us (600 so).
+// tokens fell to the last pairs and the call took 1520 us (580 so).
 constexpr int kItemUnits = 2;
 
 struct PlanArgs {
