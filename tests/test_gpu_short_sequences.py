@@ -64,3 +64,21 @@ def test_short_rejected_and_not_a_number(heads):
     assert torch.equal(got[same], o[same]) and torch.equal(got_l[same], lse[same])
     assert not bool(got[3].any()) and bool((got_l[3] == -float("inf")).all())
     assert bool(got[9].isnan().all()) and bool(got_l[9].isnan().all())
+
+
+@pytest.mark.parametrize("d,B,shared", [(P.with_(n_heads=16), 20, 40), (P, 5, 3), (P.with_(n_heads=1), 300, 2), (R, 16, 40),
+                                        (R.with_(d_c=256, page_size=32), 4, 3)],
+                         ids=["packed", "h128", "plan-kernel", "narrow", "generic"])
+def test_a_batch_of_rejected_sequences_only(d, B, shared):
+    """Every length is zero: outputs of zeros, lse of -inf, the error recorded, nothing left in the way."""
+    c = Case(d, batch(B, shared * d.page_size, [1, 70]), shared, seed=9)
+    good, good_l = c.run()
+    assert M.read_device_status() == 0
+    kept = c.lens.clone()
+    c.lens.zero_()
+    o, lse = c.run()
+    assert M.read_device_status() == -8
+    assert not bool(o.any()) and bool((lse == -float("inf")).all())
+    c.lens.copy_(kept)
+    o, lse = c.run()
+    assert M.read_device_status() == 0 and torch.equal(o, good) and torch.equal(lse, good_l)

@@ -10,7 +10,7 @@ from mla_latent_kv_42_b200 import build, synth
 pytestmark = pytest.mark.gpu
 
 P = synth.PRODUCTION.with_(d_model=1024, d_cq=256, n_heads=80)
-H16 = P.with_(n_heads=16)
+H20 = P.with_(n_heads=20)
 R = synth.RUNNING
 
 
@@ -49,19 +49,19 @@ class State:
 
 
 CALLS = {
-    "append_kv": (H16, lambda s, **k: M.append_kv(s.d, s.h, s.w["w_dkv_kr"], s.seq, s.pos, s.table, s.pool, **k)),
+    "append_kv": (H20, lambda s, **k: M.append_kv(s.d, s.h, s.w["w_dkv_kr"], s.seq, s.pos, s.table, s.pool, **k)),
     "append_kv_fp8": (P, lambda s, **k: M.append_kv_fp8(s.d, s.h, s.w["w_dkv_kr"], s.seq, s.pos, s.table, s.pool8, **k)),
-    "absorb_query": (H16, lambda s, **k: M.absorb_query(s.d, s.h, s.w["w_dq"], s.w["w_uq_qr"], s.w["w_uk"], s.pos, **k)),
+    "absorb_query": (H20, lambda s, **k: M.absorb_query(s.d, s.h, s.w["w_dq"], s.w["w_uq_qr"], s.w["w_uk"], s.pos, **k)),
     "decode": (P, lambda s, **k: M.decode_attention(s.d, s.q, s.pool, s.table, s.lens, s.n, **k)),
     "decode_narrow": (R, lambda s, **k: M.decode_attention(s.d, s.q, s.pool, s.table, s.lens, s.n, **k)),
     "decode_fp8": (P, lambda s, **k: M.decode_attention_fp8(s.d, s.q, s.pool8, s.table, s.lens, s.n, **k)),
     "prefill": (P, lambda s, **k: M.prefill_attention(s.d, s.q, s.pool, s.table, s.seq, s.pos, s.n, **k)),
-    "out_proj": (H16, lambda s, **k: M.out_proj(s.d, s.o, s.w["w_uv"], s.w["w_o"], **k)),
+    "out_proj": (H20, lambda s, **k: M.out_proj(s.d, s.o, s.w["w_uv"], s.w["w_o"], **k)),
     "read_kv": (P, lambda s, **k: M.read_kv(s.d, s.pool, s.all_seq, s.all_pos, s.table, **k)),
     "read_kv_fp8": (P, lambda s, **k: M.read_kv_fp8(s.d, s.pool8, s.all_seq, s.all_pos, s.table, **k)),
-    "shared": (H16, lambda s, **k: M.shared_prefix_attention(s.d, s.q, s.pool, s.table, s.lens, s.n, s.shared, **k)),
+    "shared": (H20, lambda s, **k: M.shared_prefix_attention(s.d, s.q, s.pool, s.table, s.lens, s.n, s.shared, **k)),
     "shared_narrow": (R, lambda s, **k: M.shared_prefix_attention(s.d, s.q, s.pool, s.table, s.lens, s.n, s.shared, **k)),
-    "layer_step": (H16, lambda s, **k: M.layer_step(M.LayerState(s.d, s.w, s.pool, s.table), s.h, s.pos, s.seq, s.lens,
+    "layer_step": (H20, lambda s, **k: M.layer_step(M.LayerState(s.d, s.w, s.pool, s.table), s.h, s.pos, s.seq, s.lens,
                                                     s.n, shared_pages=s.shared, **k)),
     "layer_step_small": (R, lambda s, **k: M.layer_step_small(M.LayerState(s.d, s.w, s.pool, s.table), s.h, s.lens, s.n,
                                                               **k)),
@@ -107,7 +107,7 @@ def test_outputs_come_from_the_streams_own_memory(name):
 
 
 def test_given_tensors_are_used_on_a_side_stream_too():
-    s, side = State(H16, 4), torch.cuda.Stream()
+    s, side = State(H20, 4), torch.cuda.Stream()
     want = M.shared_prefix_attention(s.d, s.q, s.pool, s.table, s.lens, s.n, s.shared)
     o, lse = (torch.empty_like(t) for t in want)
     side.wait_stream(torch.cuda.current_stream())
